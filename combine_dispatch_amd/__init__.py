@@ -8,7 +8,13 @@ missing or the device is not gfx950 the calls raise.
 Names match the C entry points: ``moe_fused_forward``,
 ``moe_fused_forward_packed``, ``moe_fused_forward_packed_noalloc``, ``moe_dispatch``,
 ``moe_combine``, ``moe_workspace_bytes``, ``moe_dispatch_workspace_bytes``,
-``moe_workspace_views``, ``moe_status_string``.
+``moe_workspace_views``, ``moe_status_string``; the router's ``moe_gate``,
+``moe_gate_backward``, ``moe_balance_loss`` (``include/moe_gate.h``); and the
+8-bit products ``moe_quantise_rows``, ``moe_quantise_weights``,
+``moe_quantise_columns``, ``moe_block_gemm``, ``moe_block_gemm_wgrad``
+(``include/moe_block8.h``).  The calls of the last two headers check their
+tensors (device, dtype, shape, density) and raise MoeError; they run on the
+tensors' device, by default on its current stream.
 """
 from __future__ import annotations
 
@@ -40,7 +46,14 @@ EXPORTED = ("moe_default_options", "moe_workspace_bytes", "moe_dispatch_workspac
             "moe_status_string", "moe_profile_start", "moe_profile_stop",
             "moe_profile_stage_name", "moe_packed_scales_bytes", "moe_pack_weight_scales",
             "moe_packed_weights_bytes", "moe_pack_weights", "moe_fused_forward_prepacked",
-            "moe_fused_forward_packed", "moe_fused_forward_packed_noalloc")
+            "moe_fused_forward_packed", "moe_fused_forward_packed_noalloc",
+            "moe_default_gate_options", "moe_gate", "moe_gate_backward", "moe_balance_workspace_bytes",
+            "moe_balance_loss", "moe_padded_rows", "moe_quantise_rows", "moe_quantise_weights",
+            "moe_quantise_columns", "moe_block_gemm", "moe_block_gemm_wgrad")
+MOE_DTYPE_F32 = 0
+MOE_DTYPE_BF16 = 1
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
 PROFILE_STAGES = 8
 
 
@@ -58,6 +71,24 @@ class MoeWorkspaceViews(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("counts", "offsets", "pool_src", "slot_to_pool", "pool_w", "pool_tok", "x_q",
                  "x_s", "pool_s", "act_q", "act_s", "l2_out", "capacity_rows")]
+
+
+class MoeGateShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32)]
+
+
+class MoeGateOptions(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("score", ctypes.c_int32), ("renormalise", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class MoeBalanceGrad(ctypes.Structure):
+    _fields_ = [("slope", ctypes.c_void_p), ("d_loss", ctypes.c_void_p), ("seq_offsets", ctypes.c_void_p),
+                ("S", ctypes.c_int32)]
+
+
+class MoeBlockShape(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("E", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -117,6 +148,25 @@ def lib():
         L.moe_profile_stop.restype = i32
         L.moe_profile_stage_name.argtypes = [i32]
         L.moe_profile_stage_name.restype = ctypes.c_char_p
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        gshp, gopt = ctypes.POINTER(MoeGateShape), ctypes.POINTER(MoeGateOptions)
+        bshp = ctypes.POINTER(MoeBlockShape)
+        L.moe_default_gate_options.restype = MoeGateOptions
+        L.moe_gate.argtypes = [gshp, gopt, vp, vp, vp, vp, vp, vp]
+        L.moe_gate_backward.argtypes = [gshp, gopt, vp, vp, vp, vp, ctypes.POINTER(MoeBalanceGrad), vp, vp]
+        L.moe_balance_workspace_bytes.argtypes = [gshp, ctypes.c_int32]
+        L.moe_balance_workspace_bytes.restype = sz
+        L.moe_balance_loss.argtypes = [gshp, gopt, vp, vp, vp, vp, ctypes.c_int32, f32, vp, vp, vp, vp, sz, vp]
+        L.moe_padded_rows.argtypes = [i64, ctypes.c_int32]
+        L.moe_padded_rows.restype = i64
+        L.moe_quantise_rows.argtypes = [i64, ctypes.c_int32, ctypes.c_int32, vp, vp, vp, vp, vp]
+        L.moe_quantise_weights.argtypes = [ctypes.c_int32] * 4 + [vp] * 6
+        L.moe_quantise_columns.argtypes = [i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp, vp, vp, vp, vp]
+        L.moe_block_gemm.argtypes = [bshp, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_block_gemm_wgrad.argtypes = [bshp, vp, vp, vp, vp, vp, vp, vp]
+        for name in ("moe_gate", "moe_gate_backward", "moe_balance_loss", "moe_quantise_rows",
+                     "moe_quantise_weights", "moe_quantise_columns", "moe_block_gemm", "moe_block_gemm_wgrad"):
+            getattr(L, name).restype = i32
         _lib = L
     return _lib
 
@@ -290,3 +340,253 @@ def moe_profile_stop() -> tuple[dict, int]:
     _check(lib().moe_profile_stop(ms, ctypes.byref(n)), "moe_profile_stop")
     names = [lib().moe_profile_stage_name(i).decode() for i in range(PROFILE_STAGES)]
     return dict(zip(names, list(ms))), int(n.value)
+
+
+# ---- router and 8-bit products (include/moe_gate.h, include/moe_block8.h) ----
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise MoeError(MOE_ERR_INVALID_ARG, what)
+
+
+def _dense(what: str, name: str, t, shape: tuple, dtypes: tuple, device) -> None:
+    """A densely packed device tensor of one of the dtypes and the shape (None: any length)."""
+    if (t.dtype not in dtypes or t.device != device or len(t.shape) != len(shape) or not t.is_contiguous()
+            or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise MoeError(MOE_ERR_INVALID_ARG,
+                       f"{what}: {name} must be a dense {' or '.join(str(d) for d in dtypes)} tensor of shape "
+                       f"{shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                       f"{'' if t.is_contiguous() else ', strided'}")
+
+
+def _on_device(what: str, t):
+    device = t.device
+    if device.type != "cuda":
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: tensors must be on the GPU, got {device}")
+    return device
+
+
+def _call(what: str, device, stream, *args) -> None:
+    """The C entry with the tensors' device current, on `stream` or that device's current one."""
+    import torch
+    fn = getattr(lib(), what)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(stream))
+    if rc != MOE_OK:
+        raise MoeError(rc, what)
+
+
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+
+
+def gate_options(score: str | int = "softmax", renormalise: bool = True, scale: float = 1.0) -> MoeGateOptions:
+    """Options of the router's calls; the dtype follows the logits of each call."""
+    if isinstance(score, str):
+        _need(score in _SCORES, f"gate_options: score {score!r}")
+        score = _SCORES[score]
+    return MoeGateOptions(MOE_DTYPE_F32, int(score), 1 if renormalise else 0, float(scale))
+
+
+def moe_default_gate_options() -> MoeGateOptions:
+    return lib().moe_default_gate_options()
+
+
+def _input_dtype(what: str, name: str, t) -> int:
+    import torch
+    if t.dtype == torch.float32:
+        return MOE_DTYPE_F32
+    _need(t.dtype == torch.bfloat16, f"{what}: {name} must be float32 or bfloat16, got {t.dtype}")
+    return MOE_DTYPE_BF16
+
+
+def _gate_call(what, logits, opts, token_mask, K):
+    import torch
+    device = _on_device(what, logits)
+    _need(logits.dim() == 2, f"{what}: logits must be [T][E]")
+    T, E = logits.shape
+    _dense(what, "logits", logits, (T, E), (logits.dtype,), device)
+    o = opts if opts is not None else MoeGateOptions(MOE_DTYPE_F32, MOE_SCORE_SOFTMAX, 1, 1.0)
+    o = MoeGateOptions(_input_dtype(what, "logits", logits), o.score, o.renormalise, o.scale)
+    if token_mask is not None:
+        _dense(what, "token_mask", token_mask, (T,), (torch.uint8, torch.bool), device)
+    return device, MoeGateShape(T, E, K), o
+
+
+def _sequences(what, seq_offsets, device) -> int:
+    import torch
+    if seq_offsets is None:
+        return 1
+    _dense(what, "seq_offsets", seq_offsets, (None,), (torch.int32,), device)
+    return seq_offsets.shape[0] - 1
+
+
+def moe_gate(logits, topk_idx, topk_w, bias=None, token_mask=None, opts=None, stream=None) -> None:
+    """topk_idx (int64), topk_w (fp32) [T][K] <- the top-k gate of logits [T][E]."""
+    import torch
+    _need(topk_idx.dim() == 2, "moe_gate: topk_idx must be [T][K]")
+    K = topk_idx.shape[1]
+    device, shape, o = _gate_call("moe_gate", logits, opts, token_mask, K)
+    _dense("moe_gate", "topk_idx", topk_idx, (shape.T, K), (torch.int64,), device)
+    _dense("moe_gate", "topk_w", topk_w, (shape.T, K), (torch.float32,), device)
+    if bias is not None:
+        _dense("moe_gate", "bias", bias, (shape.E,), (torch.float32,), device)
+    _call("moe_gate", device, stream, shape, o, _ptr(logits), _ptr(bias), _ptr(token_mask), _ptr(topk_idx),
+          _ptr(topk_w))
+
+
+def moe_gate_backward(logits, dlogits, topk_idx=None, d_topk_w=None, slope=None, d_loss=None, seq_offsets=None,
+                      token_mask=None, opts=None, stream=None) -> None:
+    """dlogits [T][E] <- the gradient through topk_w (topk_idx, d_topk_w) and / or
+    through the balance loss (slope of moe_balance_loss, d_loss [1] on the device)."""
+    import torch
+    what = "moe_gate_backward"
+    _need((topk_idx is None) == (d_topk_w is None), f"{what}: topk_idx and d_topk_w go together")
+    _need((slope is None) == (d_loss is None), f"{what}: slope and d_loss go together")
+    K = topk_idx.shape[-1] if topk_idx is not None else 1
+    device, shape, o = _gate_call(what, logits, opts, token_mask, K)
+    _dense(what, "dlogits", dlogits, (shape.T, shape.E), (logits.dtype,), device)
+    if topk_idx is not None:
+        _dense(what, "topk_idx", topk_idx, (shape.T, K), (torch.int64,), device)
+        _dense(what, "d_topk_w", d_topk_w, (shape.T, K), (torch.float32,), device)
+    balance = None
+    if slope is not None:
+        S = _sequences(what, seq_offsets, device)
+        _dense(what, "slope", slope, (S, shape.E), (torch.float32,), device)
+        _dense(what, "d_loss", d_loss, (1,), (torch.float32,), device)
+        balance = MoeBalanceGrad(_ptr(slope), _ptr(d_loss), _ptr(seq_offsets), S)
+    _call(what, device, stream, shape, o, _ptr(logits), _ptr(token_mask), _ptr(topk_idx), _ptr(d_topk_w), balance,
+          _ptr(dlogits))
+
+
+def moe_balance_workspace_bytes(T: int, E: int, K: int, S: int = 1) -> int:
+    return int(lib().moe_balance_workspace_bytes(MoeGateShape(T, E, K), S))
+
+
+def moe_balance_loss(logits, topk_idx, coef: float, loss, counts, slope, workspace, seq_offsets=None,
+                     token_mask=None, opts=None, stream=None) -> None:
+    """loss [1], counts (int32) and slope (fp32) [S][E] <- the balance loss of
+    logits [T][E] with the choices topk_idx [T][K]."""
+    import torch
+    what = "moe_balance_loss"
+    _need(topk_idx.dim() == 2, f"{what}: topk_idx must be [T][K]")
+    K = topk_idx.shape[1]
+    device, shape, o = _gate_call(what, logits, opts, token_mask, K)
+    S = _sequences(what, seq_offsets, device)
+    _dense(what, "topk_idx", topk_idx, (shape.T, K), (torch.int64,), device)
+    _dense(what, "loss", loss, (1,), (torch.float32,), device)
+    _dense(what, "counts", counts, (S, shape.E), (torch.int32,), device)
+    _dense(what, "slope", slope, (S, shape.E), (torch.float32,), device)
+    _dense(what, "workspace", workspace, (None,), (torch.uint8,), device)
+    _call(what, device, stream, shape, o, _ptr(logits), _ptr(token_mask), _ptr(topk_idx), _ptr(seq_offsets), S,
+          float(coef), _ptr(loss), _ptr(counts), _ptr(slope), _ptr(workspace), workspace.shape[0])
+
+
+def moe_padded_rows(R: int, E: int = 1) -> int:
+    """Rows R' of the columns layout for R rows in E groups."""
+    return int(lib().moe_padded_rows(R, E))
+
+
+def _up128(n: int) -> int:
+    return (n + 127) // 128 * 128
+
+
+def _code_types():
+    import torch
+    return (torch.uint8, torch.float8_e4m3fn)
+
+
+def moe_quantise_rows(x, codes, scales, rows_used=None, stream=None) -> None:
+    """codes [R][C'], scales fp32 [C'/128][R] <- x [R][C] (float32 or bfloat16)."""
+    import torch
+    what = "moe_quantise_rows"
+    device = _on_device(what, x)
+    _need(x.dim() == 2, f"{what}: x must be [R][C]")
+    R, C = x.shape
+    _dense(what, "x", x, (R, C), (x.dtype,), device)
+    _dense(what, "codes", codes, (R, _up128(C)), _code_types(), device)
+    _dense(what, "scales", scales, (_up128(C) // 128, R), (torch.float32,), device)
+    if rows_used is not None:
+        _dense(what, "rows_used", rows_used, (1,), (torch.int32,), device)
+    _call(what, device, stream, R, C, _input_dtype(what, "x", x), _ptr(x), _ptr(rows_used), _ptr(codes), _ptr(scales))
+
+
+def moe_quantise_weights(w, codes, scales, codes_t=None, scales_t=None, stream=None) -> None:
+    """codes [E][N][K'], scales fp32 [E][N'/128][K'/128] <- w [E][N][K]; with
+    codes_t [E][K][N'], scales_t [E][K'/128][N'/128] those of the transpose too."""
+    import torch
+    what = "moe_quantise_weights"
+    device = _on_device(what, w)
+    _need(w.dim() == 3, f"{what}: w must be [E][N][K]")
+    E, N, K = w.shape
+    Np, Kp = _up128(N), _up128(K)
+    _dense(what, "w", w, (E, N, K), (w.dtype,), device)
+    _dense(what, "codes", codes, (E, N, Kp), _code_types(), device)
+    _dense(what, "scales", scales, (E, Np // 128, Kp // 128), (torch.float32,), device)
+    _need((codes_t is None) == (scales_t is None), f"{what}: codes_t and scales_t go together")
+    if codes_t is not None:
+        _dense(what, "codes_t", codes_t, (E, K, Np), _code_types(), device)
+        _dense(what, "scales_t", scales_t, (E, Kp // 128, Np // 128), (torch.float32,), device)
+    _call(what, device, stream, E, N, K, _input_dtype(what, "w", w), _ptr(w), _ptr(codes), _ptr(scales),
+          _ptr(codes_t), _ptr(scales_t))
+
+
+def _groups(what, offsets, device) -> int:
+    import torch
+    if offsets is None:
+        return 1
+    _dense(what, "offsets", offsets, (None,), (torch.int32,), device)
+    return offsets.shape[0] - 1
+
+
+def moe_quantise_columns(x, codes, scales, offsets=None, stream=None) -> None:
+    """codes [C][R'], UE8M0 scales [R'/128][C] <- x [R][C], R' = moe_padded_rows(R, E)."""
+    import torch
+    what = "moe_quantise_columns"
+    device = _on_device(what, x)
+    _need(x.dim() == 2, f"{what}: x must be [R][C]")
+    R, C = x.shape
+    E = _groups(what, offsets, device)
+    Rp = moe_padded_rows(R, E)
+    _dense(what, "x", x, (R, C), (x.dtype,), device)
+    _dense(what, "codes", codes, (C, Rp), _code_types(), device)
+    _dense(what, "scales", scales, (Rp // 128, C), (torch.uint8,), device)
+    _call(what, device, stream, R, C, E, _input_dtype(what, "x", x), _ptr(x), _ptr(offsets), _ptr(codes), _ptr(scales))
+
+
+def moe_block_gemm(a, a_scales, w, w_scales, out, offsets=None, stream=None) -> None:
+    """out [R][N] (bf16) <- the grouped product of the quantised rows a [R][K] and weights w [E][N][K]."""
+    import torch
+    what = "moe_block_gemm"
+    device = _on_device(what, a)
+    _need(a.dim() == 2 and w.dim() == 3, f"{what}: a must be [R][K] and w [E][N][K]")
+    (R, K), (E, N) = a.shape, w.shape[:2]
+    _need(_groups(what, offsets, device) == E, f"{what}: offsets must hold E + 1 = {E + 1} entries (none: E = 1)")
+    _dense(what, "a", a, (R, K), _code_types(), device)
+    _dense(what, "a_scales", a_scales, (_up128(K) // 128, R), (torch.float32,), device)
+    _dense(what, "w", w, (E, N, K), _code_types(), device)
+    _dense(what, "w_scales", w_scales, (E, _up128(N) // 128, _up128(K) // 128), (torch.float32,), device)
+    _dense(what, "out", out, (R, N), (torch.bfloat16, torch.int16), device)
+    _call(what, device, stream, MoeBlockShape(R, N, K, E), _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales),
+          _ptr(offsets), _ptr(out))
+
+
+def moe_block_gemm_wgrad(g, g_scales, x, x_scales, out, rows: int, offsets=None, stream=None) -> None:
+    """out [E][N][K] (bf16) <- per group the product of the gradient's columns g [N][R'] and the input's x [K][R'];
+    rows: R, the rows the columns layouts were made from."""
+    import torch
+    what = "moe_block_gemm_wgrad"
+    device = _on_device(what, g)
+    E = _groups(what, offsets, device)
+    Rp = moe_padded_rows(rows, E)
+    _need(g.dim() == 2 and x.dim() == 2, f"{what}: g must be [N][R'] and x [K][R']")
+    N, K = g.shape[0], x.shape[0]
+    _dense(what, "g", g, (N, Rp), _code_types(), device)
+    _dense(what, "g_scales", g_scales, (Rp // 128, N), (torch.uint8,), device)
+    _dense(what, "x", x, (K, Rp), _code_types(), device)
+    _dense(what, "x_scales", x_scales, (Rp // 128, K), (torch.uint8,), device)
+    _dense(what, "out", out, (E, N, K), (torch.bfloat16, torch.int16), device)
+    _call(what, device, stream, MoeBlockShape(rows, N, K, E), _ptr(g), _ptr(g_scales), _ptr(x), _ptr(x_scales),
+          _ptr(offsets), _ptr(out))

@@ -9,6 +9,7 @@
 
 #include "../../include/moe.h"
 #include "../../include/moe_profile.h"
+#include "moe_host.hpp"
 #include "moe_kernels.hpp"
 
 namespace {
@@ -118,33 +119,12 @@ void launch_pack_scales(const moe_shape_t* s, const uint8_t* S1, const uint8_t* 
                        H, I / 128);
 }
 
-// gfx950 check, cached per device.
-int device_ok() {
-    static int cache[64];  // 0 unknown, 1 ok, 2 bad
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 0;
-    if (dev < 64 && cache[dev]) return cache[dev] == 1;
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return 0;
-    const int ok = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    if (dev < 64) cache[dev] = ok ? 1 : 2;
-    return ok;
-}
-
 // Workgroups of a persistent GEMM launch: one per CU (at most one fits, by
 // LDS), a multiple of 8 so that every XCD gets the same number, no more than
 // there can be tiles, and enough that no workgroup gets more than kTileCache
 // tiles (workgroups beyond the CU count then wait for a free CU).
 unsigned gemm_grid(int64_t max_tiles) {
-    static int cus[64];
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) dev = 0;
-    int n = dev < 64 ? cus[dev] : 0;
-    if (n <= 0) {
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 8)
-            n = 8;
-        if (dev < 64) cus[dev] = n;
-    }
+    const int n = device_cus();
     int64_t w = n / 8 * 8;
     const int64_t need = (max_tiles + 7) / 8 * 8;
     if (need < w) w = need;
@@ -153,8 +133,6 @@ unsigned gemm_grid(int64_t max_tiles) {
     if (w < min_w) w = min_w;
     return (unsigned)(w < 8 ? 8 : w);
 }
-
-int launch_status() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE; }
 
 // ---- optional per-kernel timing (moe_profile.h) ------------------------------
 struct Profile {

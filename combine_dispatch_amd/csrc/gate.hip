@@ -1,0 +1,876 @@
+// gate.hip -- the router's operators (include/moe_gate.h): top-k gate, its
+// gradient, the balance loss and its gradient.
+//
+// All kernels give one token row to 16 lanes (a DPP row): lane j keeps
+// VPL = ceil(E / 16) logits in registers, so four rows run in a wave and every
+// cross-lane step is four DPP rotations inside the row, with no LDS and no
+// barrier.  What bounds them: at training sizes one read of the logits (and
+// one write of the gradient) against HBM; at decode sizes the launch and the
+// chain of K dependent selections.
+#include "../../include/moe_gate.h"
+#include "moe_device.hpp"
+#include "moe_host.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kRowLanes = 16;
+constexpr int kThreads = 256;
+constexpr int kRowsPerBlock = kThreads / kRowLanes;
+constexpr int kMaxSlots = 4;  // slots per lane: K <= 64
+
+// ---- steps across the 16 lanes of a row ------------------------------------
+template <int N>
+__device__ __forceinline__ uint32_t ror(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x120 + N, 0xF, 0xF, false);
+}
+template <int N>
+__device__ __forceinline__ float ror(float v) {
+    return __uint_as_float(ror<N>(__float_as_uint(v)));
+}
+__device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin2(uint32_t a, uint32_t b) { return a < b ? a : b; }
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+    v = umax2(v, ror<8>(v));
+    v = umax2(v, ror<4>(v));
+    v = umax2(v, ror<2>(v));
+    return umax2(v, ror<1>(v));
+}
+__device__ __forceinline__ uint32_t row_min(uint32_t v) {
+    v = umin2(v, ror<8>(v));
+    v = umin2(v, ror<4>(v));
+    v = umin2(v, ror<2>(v));
+    return umin2(v, ror<1>(v));
+}
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, ror<8>(v));
+    v = fmaxf(v, ror<4>(v));
+    v = fmaxf(v, ror<2>(v));
+    return fmaxf(v, ror<1>(v));
+}
+// The same bits in every lane: each step adds the same two values in one of
+// the two orders.
+__device__ __forceinline__ float row_sum(float v) {
+    v += ror<8>(v);
+    v += ror<4>(v);
+    v += ror<2>(v);
+    return v + ror<1>(v);
+}
+
+// ---- a row's logits ----------------------------------------------------------
+// Lane j's value i is expert ((i / VEC) * 16 + j) * VEC + i % VEC: VEC wide
+// loads, ascending in i.  Experts past E read as -inf.
+template <int VEC>
+__device__ __forceinline__ int expert_of(int i, int j) {
+    return ((i / VEC) * kRowLanes + j) * VEC + i % VEC;
+}
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<MOE_DTYPE_F32> {
+    typedef float type;
+    static __device__ __forceinline__ float get(float v) { return v; }
+    static __device__ __forceinline__ float put(float v) { return v; }
+};
+template <>
+struct Elem<MOE_DTYPE_BF16> {
+    typedef uint16_t type;
+    static __device__ __forceinline__ float get(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+    static __device__ __forceinline__ uint16_t put(float v) { return (uint16_t)pack_bf16x2(v, 0.f); }
+};
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+    T v[VEC];
+};
+
+template <int DT, int VPL, int VEC>
+__device__ __forceinline__ void load_row(const typename Elem<DT>::type* row, int E, int j, float (&v)[VPL]) {
+    typedef Pack<typename Elem<DT>::type, VEC> P;
+#pragma unroll
+    for (int i = 0; i < VPL; i += VEC) {
+        const int e = expert_of<VEC>(i, j);
+        if (e < E) {  // E % VEC == 0: all or none
+            const P p = *reinterpret_cast<const P*>(row + e);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) v[i + c] = Elem<DT>::get(p.v[c]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) v[i + c] = -INFINITY;
+        }
+    }
+}
+
+template <int DT, int VPL, int VEC>
+__device__ __forceinline__ void store_row(typename Elem<DT>::type* row, int E, int j, const float (&v)[VPL]) {
+    typedef Pack<typename Elem<DT>::type, VEC> P;
+#pragma unroll
+    for (int i = 0; i < VPL; i += VEC) {
+        const int e = expert_of<VEC>(i, j);
+        if (e < E) {
+            P p;
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) p.v[c] = Elem<DT>::put(v[i + c]);
+            *reinterpret_cast<P*>(row + e) = p;
+        }
+    }
+}
+
+__device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
+__device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-(double)l)); }
+
+// An unsigned key in the order of v: -0 = +0, NaN above all, never 0 (0 marks
+// what cannot be chosen: -inf and experts past E).
+__device__ __forceinline__ uint32_t order_key(float v) {
+    if (v != v) return 0xFFFFFFFFu;
+    const uint32_t b = __float_as_uint(v + 0.f);
+    const uint32_t k = b ^ ((int32_t)b < 0 ? 0xFFFFFFFFu : 0x80000000u);
+    return v == -INFINITY ? 0u : k;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k ^ ((int32_t)k < 0 ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ uint64_t order_key64(double v) {
+    if (v != v) return ~0ull;
+    const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+    const uint64_t k = b ^ ((int64_t)b < 0 ? ~0ull : 0x8000000000000000ull);
+    return v == -INFINITY ? 0ull : k;
+}
+
+// ---- top-k gate --------------------------------------------------------------
+// K rounds of: the lane's largest key, the row's largest (4 DPP steps), the
+// lowest expert holding it (4 more), taken out.  Without a bias the key is the
+// logit itself, so the choice is exact.  With a bias the key is
+// sigmoid + bias: float32 first, and where two neighbours among the first
+// K + 1 lie within kNear of each other (a few tokens in a thousand) the row is
+// chosen again by float64 keys.  kNear: the float32 key is off by at most
+// 2^-22 (exp and division: 4 half-steps of a value below 1) plus half a step
+// of the sum, 2^-24 (1 + |key|); two keys' errors are below
+// 2^-20 (1 + |key|).
+template <int DT, int VPL, int VEC, bool BIAS>
+__global__ __launch_bounds__(kThreads) void k_gate(const typename Elem<DT>::type* __restrict__ logits,
+                                                   const float* __restrict__ bias,
+                                                   const uint8_t* __restrict__ mask, int T, int E, int K,
+                                                   int score, int renorm, float scale,
+                                                   int64_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
+    const int j = threadIdx.x & (kRowLanes - 1);
+    const int64_t t = (int64_t)blockIdx.x * kRowsPerBlock + threadIdx.x / kRowLanes;
+    if (t >= T) return;  // whole rows of lanes leave together
+    const typename Elem<DT>::type* row = logits + t * E;
+    int64_t* idx_out = topk_idx + t * K;
+    float* w_out = topk_w + t * K;
+    if (mask && !mask[t]) {
+        for (int k = j; k < K; k += kRowLanes) {
+            idx_out[k] = -1;
+            w_out[k] = 0.f;
+        }
+        return;
+    }
+
+    uint32_t key[VPL];
+    float top = 0.f, total = 1.f;  // softmax over all experts: largest logit, sum of exp
+    {
+        float v[VPL];
+        load_row<DT, VPL, VEC>(row, E, j, v);
+        if (score == MOE_SCORE_SOFTMAX && !renorm) {
+            top = v[0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) top = fmaxf(top, v[i]);
+            top = row_max(top);
+            total = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) total += expf(v[i] - top);
+            total = row_sum(total);
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            float s = v[i];
+            if (BIAS) {
+                const int e = expert_of<VEC>(i, j);
+                s = v[i] == -INFINITY ? v[i] : sigmoid(v[i]) + (e < E ? bias[e] : 0.f);
+            }
+            key[i] = order_key(s);
+        }
+    }
+
+    int sel[kMaxSlots] = {-1, -1, -1, -1};
+    bool near = false;
+    float last = 0.f;
+    const int rounds = BIAS && K < E ? K + 1 : K;
+#pragma unroll
+    for (int b = 0; b <= kMaxSlots; ++b) {  // the fifth: only the extra round of K = 64
+#pragma unroll 1
+        for (int k = b * kRowLanes; k < rounds && k < (b + 1) * kRowLanes; ++k) {
+            uint32_t m = key[0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) m = umax2(m, key[i]);
+            m = row_max(m);
+            if (BIAS) {
+                const float s = key_value(m);
+                near |= k > 0 && m != 0 && last - s <= 0x1p-20f * (1.f + fabsf(s));
+                last = s;
+                if (k == K) break;
+            }
+            uint32_t at = 0x7FFFFFFFu;
+#pragma unroll
+            for (int i = VPL - 1; i >= 0; --i) at = key[i] == m ? (uint32_t)expert_of<VEC>(i, j) : at;
+            at = row_min(at);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) key[i] = expert_of<VEC>(i, j) == (int)at ? 0u : key[i];
+            if (b < kMaxSlots && (k & (kRowLanes - 1)) == j) sel[b < kMaxSlots ? b : 0] = m ? (int)at : -1;
+        }
+    }
+
+    if (BIAS && near) {
+        uint32_t hi[VPL], lo[VPL];
+        float v[VPL];
+        load_row<DT, VPL, VEC>(row, E, j, v);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = expert_of<VEC>(i, j);
+            const uint64_t k64 = v[i] == -INFINITY ? 0ull : order_key64(sigmoid64(v[i]) + (double)(e < E ? bias[e] : 0.f));
+            hi[i] = (uint32_t)(k64 >> 32);
+            lo[i] = (uint32_t)k64;
+        }
+#pragma unroll
+        for (int b = 0; b < kMaxSlots; ++b) {
+#pragma unroll 1
+            for (int k = b * kRowLanes; k < K && k < (b + 1) * kRowLanes; ++k) {
+                uint32_t mh = hi[0];
+#pragma unroll
+                for (int i = 1; i < VPL; ++i) mh = umax2(mh, hi[i]);
+                mh = row_max(mh);
+                uint32_t ml = 0;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) ml = umax2(ml, hi[i] == mh ? lo[i] : 0u);
+                ml = row_max(ml);
+                uint32_t at = 0x7FFFFFFFu;
+#pragma unroll
+                for (int i = VPL - 1; i >= 0; --i)
+                    at = hi[i] == mh && lo[i] == ml ? (uint32_t)expert_of<VEC>(i, j) : at;
+                at = row_min(at);
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    const bool gone = expert_of<VEC>(i, j) == (int)at;
+                    hi[i] = gone ? 0u : hi[i];
+                    lo[i] = gone ? 0u : lo[i];
+                }
+                if ((k & (kRowLanes - 1)) == j) sel[b] = (mh | ml) ? (int)at : -1;
+            }
+        }
+    }
+
+    // weights of the chosen: lane j holds slots j, j + 16, ...
+    float s[kMaxSlots];
+    float chosen_top = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < kMaxSlots; ++b) {
+        s[b] = sel[b] >= 0 ? Elem<DT>::get(row[sel[b]]) : -INFINITY;
+        chosen_top = fmaxf(chosen_top, s[b]);
+    }
+    if (score == MOE_SCORE_SOFTMAX && renorm) top = row_max(chosen_top);
+    float sum = 0.f;
+#pragma unroll
+    for (int b = 0; b < kMaxSlots; ++b) {
+        s[b] = sel[b] < 0 ? 0.f : score == MOE_SCORE_SIGMOID ? sigmoid(s[b]) : expf(s[b] - top);
+        sum += s[b];
+    }
+    if (renorm) total = row_sum(sum);
+#pragma unroll
+    for (int b = 0; b < kMaxSlots; ++b) {
+        const int k = b * kRowLanes + j;
+        if (k < K) {
+            const float w = total == 0.f ? 0.f : s[b] / total;
+            idx_out[k] = sel[b];
+            w_out[k] = sel[b] < 0 ? 0.f : scale * w;
+        }
+    }
+}
+
+// ---- sequences -----------------------------------------------------------------
+__device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+// The tokens [lo, hi) of sequence q, kept inside 0..T whatever the offsets hold.
+__device__ __forceinline__ void sequence_range(const int32_t* off, int q, int T, int& lo, int& hi) {
+    lo = off ? clamp_int(off[q], 0, T) : 0;
+    hi = off ? clamp_int(off[q + 1], lo, T) : T;
+}
+
+// The first sequence that ends behind token t (S if none), searched by the 16
+// lanes of a row together: 16 pivots a step.
+__device__ __forceinline__ int sequence_of(const int32_t* off, int S, int t, int j) {
+    int lo = 0, n = S;
+    while (n > 0) {
+        const int step = (n + kRowLanes - 1) / kRowLanes;
+        const int i = lo + j * step;
+        const bool passed = j * step < n && off[i + 1] <= t;
+        const uint32_t c = row_max(passed ? (uint32_t)(j + 1) : 0u);
+        if (c == 0) break;
+        const int at = ((int)c - 1) * step + 1;  // sequences of this span known to end before t
+        lo += at;
+        n = (step - 1 < n - at) ? step - 1 : n - at;
+    }
+    return lo;
+}
+
+// ---- gradient --------------------------------------------------------------------
+// With g_j = scale * d_topk_w of the chosen experts j, q_j = s_j / sum of the
+// chosen s, p = the softmax (or s / sum of s) over all experts and f_e =
+// d_loss * slope_e of the token's sequence:
+//   softmax, renormalised    dl_j = q_j (g_j - sum g q)
+//   softmax                  dl_e = p_e (g_e - sum g p)           (g = 0 where not chosen)
+//   sigmoid, renormalised    dl_j = q_j (1 - s_j) (g_j - sum g q)
+//   sigmoid                  dl_j = g_j s_j (1 - s_j)
+//   balance, softmax         dl_e += p_e (f_e - sum f p)
+//   balance, sigmoid         dl_e += p_e (1 - s_e) (f_e - sum f p)
+// The chosen experts' terms reach the lanes that own them through one LDS row
+// per token (an atomic add each, different addresses unless the caller names
+// an expert twice), private to the 16 lanes of one wave: no barrier.  The rows
+// lie 16 words apart modulo the 64 banks, so a wave's four rows do not collide
+// (not for VPL = 64, whose 16 rows fill 64 KiB as they are).
+template <int VPL>
+constexpr int kGradRow = kRowLanes * VPL + (VPL < 64 ? kRowLanes : 0);
+
+template <int DT, int VPL, int VEC>
+__global__ __launch_bounds__(kThreads) void k_gate_backward(
+    const typename Elem<DT>::type* __restrict__ logits, const uint8_t* __restrict__ mask, int T, int E, int K,
+    int score, int renorm, float scale, const int64_t* __restrict__ topk_idx, const float* __restrict__ d_topk_w,
+    const float* __restrict__ slope, const float* __restrict__ d_loss, const int32_t* __restrict__ seq_offsets,
+    int S, typename Elem<DT>::type* __restrict__ dlogits) {
+    extern __shared__ float lds_rows[];
+    const int j = threadIdx.x & (kRowLanes - 1);
+    const int64_t t = (int64_t)blockIdx.x * kRowsPerBlock + threadIdx.x / kRowLanes;
+    if (t >= T) return;
+    const typename Elem<DT>::type* row = logits + t * E;
+    float d[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) d[i] = 0.f;
+    if (mask && !mask[t]) {
+        store_row<DT, VPL, VEC>(dlogits + t * E, E, j, d);
+        return;
+    }
+    int q = 0;
+    bool counted = slope != nullptr;
+    if (slope && seq_offsets) {
+        q = sequence_of(seq_offsets, S, (int)t, j);
+        counted = q < S && seq_offsets[q < S ? q : 0] <= (int)t;
+    }
+
+    // the chosen slots' logits, before the whole row's work
+    int at[kMaxSlots];
+    float g[kMaxSlots], l[kMaxSlots];
+#pragma unroll
+    for (int b = 0; b < kMaxSlots; ++b) {
+        const int k = b * kRowLanes + j;
+        at[b] = -1;
+        g[b] = 0.f;
+        if (topk_idx && k < K) {
+            const int64_t e = topk_idx[t * K + k];
+            if (e >= 0 && e < E) {
+                at[b] = (int)e;
+                g[b] = scale * d_topk_w[t * K + k];
+            }
+        }
+        l[b] = at[b] >= 0 ? Elem<DT>::get(row[at[b]]) : -INFINITY;
+    }
+
+    float v[VPL];
+    load_row<DT, VPL, VEC>(row, E, j, v);
+    // scores over all experts: v = exp(l - top) or sigmoid(l), total = their sum
+    const bool soft = score == MOE_SCORE_SOFTMAX;
+    const bool whole = counted || (soft && !renorm);
+    float top = 0.f, total = 1.f;
+    if (whole) {
+        if (soft) {
+            top = v[0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) top = fmaxf(top, v[i]);
+            top = row_max(top);
+            top = top == -INFINITY ? 0.f : top;  // no expert at all: every exp is 0
+        }
+        total = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            v[i] = soft ? expf(v[i] - top) : sigmoid(v[i]);
+            total += v[i];
+        }
+        total = row_sum(total);
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+
+    if (topk_idx) {
+        float s[kMaxSlots], sum = 0.f, dot = 0.f;
+        if (soft && renorm) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < kMaxSlots; ++b) m = fmaxf(m, l[b]);
+            top = row_max(m);
+        }
+#pragma unroll
+        for (int b = 0; b < kMaxSlots; ++b) {
+            s[b] = at[b] < 0 ? 0.f : soft ? expf(l[b] - top) : sigmoid(l[b]);
+            sum += s[b];
+        }
+        float over = inv;
+        if (renorm) {
+            sum = row_sum(sum);
+            over = sum == 0.f ? 0.f : 1.f / sum;
+        } else if (!soft) {
+            over = 1.f;
+        }
+        if (renorm || soft) {
+#pragma unroll
+            for (int b = 0; b < kMaxSlots; ++b) dot += at[b] < 0 ? 0.f : g[b] * (s[b] * over);
+            dot = row_sum(dot);
+        }
+        float* buf = lds_rows + (threadIdx.x / kRowLanes) * kGradRow<VPL>;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) buf[i * kRowLanes + j] = 0.f;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int b = 0; b < kMaxSlots; ++b) {
+            if (at[b] >= 0) {
+                float term;
+                if (soft && !renorm)
+                    term = (s[b] * over) * g[b];
+                else
+                    term = (s[b] * over) * (g[b] - dot) * (soft ? 1.f : 1.f - s[b]);
+                // expert e = (m * 16 + lane) * VEC + c sits at value m * VEC + c of its lane
+                const int e = at[b], m = e / (kRowLanes * VEC), ln = e / VEC % kRowLanes, c = e % VEC;
+                atomicAdd(&buf[(m * VEC + c) * kRowLanes + ln], term);
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) d[i] = buf[i * kRowLanes + j];
+        if (soft && !renorm) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) d[i] -= v[i] * inv * dot;
+        }
+    }
+
+    if (counted) {
+        const float dl = d_loss[0];
+        const float* f_row = slope + (int64_t)q * E;
+        float dot = 0.f;
+        float f[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = expert_of<VEC>(i, j);
+            f[i] = e < E ? dl * f_row[e] : 0.f;
+            dot += f[i] * (v[i] * inv);
+        }
+        dot = row_sum(dot);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) d[i] += (v[i] * inv) * (f[i] - dot) * (soft ? 1.f : 1.f - v[i]);
+    }
+    store_row<DT, VPL, VEC>(dlogits + t * E, E, j, d);
+}
+
+// ---- balance loss -----------------------------------------------------------------
+// Two launches.  k_balance_part: a block per chunk of kChunk tokens adds up,
+// for each sequence q that the chunk b meets, the probabilities and the slot
+// counts of every expert into row b + q of the partial tables.  Going through
+// the pairs (b, q) in token order each step raises b or q, so the rows differ,
+// there are at most chunks + S of them, and no float atomics are needed.
+// k_balance_final: blocks over (sequence, 16 experts) add the rows; the last
+// block to finish adds the blocks' losses in a fixed order.
+constexpr int kChunk = 32;
+constexpr int kFinalThreads = 512;
+constexpr int kFinalBlocks = 512;
+constexpr int kFinalExperts = 16;
+
+struct BalanceWs {
+    uint32_t* arrived;  // blocks of k_balance_final that are done (cleared by k_balance_part)
+    double* loss_part;  // [kFinalBlocks]
+    int2* pair_n;       // [chunks + S]: live tokens, counted slots
+    float* part_p;      // [chunks + S][E]
+    int32_t* part_c;    // [chunks + S][E]
+};
+
+template <int DT, int VPL, int VEC>
+__global__ __launch_bounds__(kThreads) void k_balance_part(
+    const typename Elem<DT>::type* __restrict__ logits, const uint8_t* __restrict__ mask,
+    const int64_t* __restrict__ topk_idx, int T, int E, int K, int score, const int32_t* __restrict__ seq_offsets,
+    int S, BalanceWs ws) {
+    extern __shared__ float lds_sum[];  // [4][E] probability sums, then [E] counts
+    __shared__ int lds_n[2];
+    int* lds_c = reinterpret_cast<int*>(lds_sum + 4 * E);
+    const int tid = threadIdx.x, j = tid & (kRowLanes - 1), wave = tid / kWave;
+    const int b = blockIdx.x;
+    if (b == 0 && tid == 0) *ws.arrived = 0;
+    const int t0 = b * kChunk, t1 = T - t0 < kChunk ? T : t0 + kChunk;
+    if (t0 >= T) return;  // T == 0
+    const bool soft = score == MOE_SCORE_SOFTMAX;
+
+    for (int q = seq_offsets ? sequence_of(seq_offsets, S, t0, j) : 0; q < S; ++q) {
+        int lo, hi;
+        sequence_range(seq_offsets, q, T, lo, hi);
+        if (lo >= t1) break;
+        lo = lo < t0 ? t0 : lo;
+        hi = hi < t1 ? hi : t1;
+        if (lo >= hi) continue;
+        __syncthreads();
+        for (int e = tid; e < E; e += kThreads) lds_c[e] = 0;
+        if (tid < 2) lds_n[tid] = 0;
+        __syncthreads();
+        int found = 0;
+        for (int i = tid; i < (hi - lo) * K; i += kThreads) {
+            const int t = lo + i / K;
+            const int64_t e = topk_idx[(int64_t)lo * K + i];
+            if (e >= 0 && e < E && !(mask && !mask[t])) {
+                atomicAdd(&lds_c[e], 1);
+                ++found;
+            }
+        }
+        if (found) atomicAdd(&lds_n[1], found);
+        float acc[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+        for (int t = lo + tid / kRowLanes; t < hi; t += kRowsPerBlock) {
+            if (mask && !mask[t]) continue;
+            if (j == 0) atomicAdd(&lds_n[0], 1);
+            float v[VPL];
+            load_row<DT, VPL, VEC>(logits + (int64_t)t * E, E, j, v);
+            float top = 0.f, total = 0.f;
+            if (soft) {
+                top = v[0];
+#pragma unroll
+                for (int i = 1; i < VPL; ++i) top = fmaxf(top, v[i]);
+                top = row_max(top);
+                top = top == -INFINITY ? 0.f : top;
+            }
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                v[i] = soft ? expf(v[i] - top) : sigmoid(v[i]);
+                total += v[i];
+            }
+            total = row_sum(total);
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) acc[i] += v[i] * inv;
+        }
+        // the wave's four rows, then the block's four waves
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            acc[i] += __shfl_xor(acc[i], 16);
+            acc[i] += __shfl_xor(acc[i], 32);
+            const int e = expert_of<VEC>(i, j);
+            if ((tid & (kWave - 1)) < kRowLanes && e < E) lds_sum[wave * E + e] = acc[i];
+        }
+        __syncthreads();
+        const int64_t at = (int64_t)(b + q) * E;
+        for (int e = tid; e < E; e += kThreads) {
+            ws.part_p[at + e] = (lds_sum[e] + lds_sum[E + e]) + (lds_sum[2 * E + e] + lds_sum[3 * E + e]);
+            ws.part_c[at + e] = lds_c[e];
+        }
+        if (tid == 0) ws.pair_n[b + q] = make_int2(lds_n[0], lds_n[1]);
+    }
+}
+
+__global__ __launch_bounds__(kFinalThreads) void k_balance_final(int T, int E, const int32_t* __restrict__ seq_offsets,
+                                                                 int S, float coef, float* __restrict__ loss,
+                                                                 int32_t* __restrict__ counts,
+                                                                 float* __restrict__ slope, BalanceWs ws,
+                                                                 int lanes_per_seq) {
+    constexpr int kSlices = kFinalThreads / kFinalExperts;
+    __shared__ double lds_p[kSlices][kFinalExperts];
+    __shared__ int lds_c[kSlices][kFinalExperts];
+    __shared__ int lds_live;
+    __shared__ int2 lds_nc;
+    __shared__ bool lds_last;
+    const int tid = threadIdx.x;
+    if (tid == 0) lds_live = 0;
+    __syncthreads();
+    // sequences with a live token: lanes_per_seq lanes (a power of two) each
+    {
+        int found = 0;
+        const int per = kFinalThreads / lanes_per_seq, ln = tid % lanes_per_seq;
+        for (int q0 = 0; q0 < S; q0 += per) {
+            const int q = q0 + tid / lanes_per_seq;
+            int n = 0;
+            if (q < S) {
+                int lo, hi;
+                sequence_range(seq_offsets, q, T, lo, hi);
+                if (lo < hi)
+                    for (int b = lo / kChunk + ln; b <= (hi - 1) / kChunk; b += lanes_per_seq) n += ws.pair_n[b + q].x;
+            }
+            for (int m = 1; m < lanes_per_seq; m <<= 1) n += __shfl_xor(n, m);
+            found += ln == 0 && n > 0;
+        }
+        if (found) atomicAdd(&lds_live, found);
+    }
+    __syncthreads();
+    const int live = lds_live;
+
+    double sum = 0.0;  // this block's share of the loss (thread 0)
+    const int eblocks = (E + kFinalExperts - 1) / kFinalExperts;
+    const int64_t items = (int64_t)S * eblocks;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int q = (int)(it / eblocks), e = (int)(it % eblocks) * kFinalExperts + tid % kFinalExperts;
+        const int sl = tid / kFinalExperts;
+        int lo, hi;
+        sequence_range(seq_offsets, q, T, lo, hi);
+        const int b0 = lo / kChunk, b1 = lo < hi ? (hi - 1) / kChunk : b0 - 1;
+        double p = 0.0;
+        int c = 0;
+        if (e < E)
+            for (int b = b0 + sl; b <= b1; b += kSlices) {
+                p += (double)ws.part_p[(int64_t)(b + q) * E + e];
+                c += ws.part_c[(int64_t)(b + q) * E + e];
+            }
+        lds_p[sl][tid % kFinalExperts] = p;
+        lds_c[sl][tid % kFinalExperts] = c;
+        if (tid < kWave) {
+            int n = 0, m = 0;
+            for (int b = b0 + tid; b <= b1; b += kWave) {
+                const int2 v = ws.pair_n[b + q];
+                n += v.x;
+                m += v.y;
+            }
+            for (int x = 1; x < kWave; x <<= 1) {
+                n += __shfl_xor(n, x);
+                m += __shfl_xor(m, x);
+            }
+            if (tid == 0) lds_nc = make_int2(n, m);
+        }
+        __syncthreads();
+        if (tid < kFinalExperts) {
+            p = 0.0;
+            c = 0;
+            for (int i = 0; i < kSlices; ++i) {
+                p += lds_p[i][tid];
+                c += lds_c[i][tid];
+            }
+            const int2 nc = lds_nc;
+            double f = 0.0;
+            if (nc.x > 0 && nc.y > 0) f = (double)coef * E * c / ((double)nc.y * nc.x * live);
+            if (e < E) {
+                counts[(int64_t)q * E + e] = c;
+                slope[(int64_t)q * E + e] = (float)f;
+            }
+            double part = e < E ? f * p : 0.0;
+            for (int x = 1; x < kFinalExperts; x <<= 1) part += __shfl_xor(part, x);
+            sum += part;
+        }
+        __syncthreads();
+    }
+    if (tid == 0) {
+        __hip_atomic_store(&ws.loss_part[blockIdx.x], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint32_t before =
+            __hip_atomic_fetch_add(ws.arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        lds_last = before == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (lds_last && tid < kWave) {
+        double all = 0.0;
+        for (int i = tid; i < (int)gridDim.x; i += kWave)
+            all += __hip_atomic_load(&ws.loss_part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        for (int x = 1; x < kWave; x <<= 1) all += __shfl_xor(all, x);
+        if (tid == 0) *loss = (float)all;
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------
+constexpr int32_t kMaxTokens = 1 << 27;  // a launch holds fewer than 2^32 threads
+bool gate_shape_ok(const moe_gate_shape_t* s) {
+    return s && s->T >= 0 && s->T <= kMaxTokens && s->E >= 1 && s->E <= 1024 && s->K >= 1 && s->K <= 64 && s->K <= s->E;
+}
+
+// 16 * VPL >= E, VPL a power of two; VEC as wide as 16 bytes where every row
+// starts on such a boundary and holds whole vectors, else single values.
+template <int DT, int VPL, typename F>
+void with_vec(int E, bool vec_ok, F f) {
+    constexpr int kMost = DT == MOE_DTYPE_F32 ? 4 : 8;
+    constexpr int V = VPL < kMost ? VPL : kMost;
+    if (V > 1 && vec_ok && E % V == 0)
+        f(std::integral_constant<int, VPL>(), std::integral_constant<int, V>());
+    else
+        f(std::integral_constant<int, VPL>(), std::integral_constant<int, 1>());
+}
+template <int DT, typename F>
+void with_row(int E, bool vec_ok, F f) {
+    if (E <= 16) with_vec<DT, 1>(E, vec_ok, f);
+    else if (E <= 32) with_vec<DT, 2>(E, vec_ok, f);
+    else if (E <= 64) with_vec<DT, 4>(E, vec_ok, f);
+    else if (E <= 128) with_vec<DT, 8>(E, vec_ok, f);
+    else if (E <= 256) with_vec<DT, 16>(E, vec_ok, f);
+    else if (E <= 512) with_vec<DT, 32>(E, vec_ok, f);
+    else with_vec<DT, 64>(E, vec_ok, f);
+}
+
+unsigned row_blocks(int T) { return (unsigned)(((int64_t)T + kRowsPerBlock - 1) / kRowsPerBlock); }
+
+template <int DT>
+void launch_gate(const moe_gate_shape_t* s, const moe_gate_options_t& o, const void* logits, const float* bias,
+                 const uint8_t* mask, int64_t* idx, float* w, hipStream_t stream) {
+    typedef typename Elem<DT>::type T;
+    with_row<DT>(s->E, aligned(logits, 16), [&](auto vpl, auto vec) {
+        constexpr int VPL = decltype(vpl)::value, VEC = decltype(vec)::value;
+        if (bias)
+            hipLaunchKernelGGL((k_gate<DT, VPL, VEC, true>), dim3(row_blocks(s->T)), dim3(kThreads), 0, stream,
+                               (const T*)logits, bias, mask, s->T, s->E, s->K, o.score, o.renormalise, o.scale, idx, w);
+        else
+            hipLaunchKernelGGL((k_gate<DT, VPL, VEC, false>), dim3(row_blocks(s->T)), dim3(kThreads), 0, stream,
+                               (const T*)logits, bias, mask, s->T, s->E, s->K, o.score, o.renormalise, o.scale, idx, w);
+    });
+}
+
+template <int DT>
+void launch_gate_backward(const moe_gate_shape_t* s, const moe_gate_options_t& o, const void* logits,
+                          const uint8_t* mask, const int64_t* idx, const float* dw, const moe_balance_grad_t& b,
+                          void* dlogits, hipStream_t stream) {
+    typedef typename Elem<DT>::type T;
+    with_row<DT>(s->E, aligned(logits, 16) && aligned(dlogits, 16), [&](auto vpl, auto vec) {
+        constexpr int VPL = decltype(vpl)::value, VEC = decltype(vec)::value;
+        const size_t lds = idx ? sizeof(float) * kRowsPerBlock * kGradRow<VPL> : 0;
+        hipLaunchKernelGGL((k_gate_backward<DT, VPL, VEC>), dim3(row_blocks(s->T)), dim3(kThreads), lds, stream,
+                           (const T*)logits, mask, s->T, s->E, s->K, o.score, o.renormalise, o.scale, idx, dw, b.slope,
+                           b.d_loss, b.seq_offsets, b.S, (T*)dlogits);
+    });
+}
+
+template <int DT>
+void launch_balance_part(const moe_gate_shape_t* s, int score, const void* logits, const uint8_t* mask,
+                         const int64_t* idx, const int32_t* seq_offsets, int S, const BalanceWs& ws, unsigned blocks,
+                         hipStream_t stream) {
+    typedef typename Elem<DT>::type T;
+    with_row<DT>(s->E, aligned(logits, 16), [&](auto vpl, auto vec) {
+        constexpr int VPL = decltype(vpl)::value, VEC = decltype(vec)::value;
+        hipLaunchKernelGGL((k_balance_part<DT, VPL, VEC>), dim3(blocks), dim3(kThreads), sizeof(float) * 5 * s->E,
+                           stream, (const T*)logits, mask, idx, s->T, s->E, s->K, score, seq_offsets, S, ws);
+    });
+}
+
+bool seq_ok(const moe_gate_shape_t* s, int32_t S) {
+    return gate_shape_ok(s) && S >= 1 && S <= 65536 && (int64_t)S * s->E < (int64_t(1) << 31);
+}
+
+size_t balance_layout(const moe_gate_shape_t* s, int32_t S, uint8_t* base, BalanceWs* ws) {
+    const size_t rows = (size_t)((s->T + (int64_t)kChunk - 1) / kChunk) + S;
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o = (o + bytes + 15) / 16 * 16;
+        return at;
+    };
+    const size_t arrived = take(sizeof(uint32_t)), loss_part = take(sizeof(double) * kFinalBlocks);
+    const size_t pair_n = take(sizeof(int2) * rows), part_p = take(sizeof(float) * rows * s->E);
+    const size_t part_c = take(sizeof(int32_t) * rows * s->E);
+    if (ws) {
+        ws->arrived = reinterpret_cast<uint32_t*>(base + arrived);
+        ws->loss_part = reinterpret_cast<double*>(base + loss_part);
+        ws->pair_n = reinterpret_cast<int2*>(base + pair_n);
+        ws->part_p = reinterpret_cast<float*>(base + part_p);
+        ws->part_c = reinterpret_cast<int32_t*>(base + part_c);
+    }
+    return o;
+}
+
+int check_options(const moe_gate_options_t* o) {
+    if (o->dtype != MOE_DTYPE_F32 && o->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+    if (o->score != MOE_SCORE_SOFTMAX && o->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+    if (o->renormalise != 0 && o->renormalise != 1) return MOE_ERR_INVALID_ARG;
+    if (!(o->scale - o->scale == 0.f)) return MOE_ERR_INVALID_ARG;  // not finite
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_gate_options_t moe_default_gate_options(void) {
+    moe_gate_options_t o;
+    o.dtype = MOE_DTYPE_F32;
+    o.score = MOE_SCORE_SOFTMAX;
+    o.renormalise = 1;
+    o.scale = 1.f;
+    return o;
+}
+
+int moe_gate(const moe_gate_shape_t* s, const moe_gate_options_t* opt, const void* logits, const float* bias,
+             const uint8_t* token_mask, int64_t* topk_idx, float* topk_w, moe_stream_t stream) {
+    const moe_gate_options_t o = opt ? *opt : moe_default_gate_options();
+    if (!s || check_options(&o) != MOE_OK) return MOE_ERR_INVALID_ARG;
+    if (!gate_shape_ok(s)) return s->T < 0 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED;
+    if (bias && o.score == MOE_SCORE_SOFTMAX) return MOE_ERR_UNSUPPORTED;
+    if (s->T == 0) return MOE_OK;
+    if (!logits || !topk_idx || !topk_w) return MOE_ERR_INVALID_ARG;
+    const size_t elem = o.dtype == MOE_DTYPE_F32 ? 4 : 2;
+    if (!aligned(logits, elem) || !aligned(topk_idx, 8) || !aligned(topk_w, 4) || !aligned(bias, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_DEVICE;
+    if (o.dtype == MOE_DTYPE_F32)
+        launch_gate<MOE_DTYPE_F32>(s, o, logits, bias, token_mask, topk_idx, topk_w, stream);
+    else
+        launch_gate<MOE_DTYPE_BF16>(s, o, logits, bias, token_mask, topk_idx, topk_w, stream);
+    return launch_status();
+}
+
+size_t moe_balance_workspace_bytes(const moe_gate_shape_t* s, int32_t S) {
+    return seq_ok(s, S) ? balance_layout(s, S, nullptr, nullptr) : 0;
+}
+
+int moe_balance_loss(const moe_gate_shape_t* s, const moe_gate_options_t* opt, const void* logits,
+                     const uint8_t* token_mask, const int64_t* topk_idx, const int32_t* seq_offsets, int32_t S,
+                     float coef, float* loss, int32_t* counts, float* slope, void* workspace,
+                     size_t workspace_bytes, moe_stream_t stream) {
+    const moe_gate_options_t o = opt ? *opt : moe_default_gate_options();
+    if (!s || check_options(&o) != MOE_OK || S < 1 || (!seq_offsets && S != 1)) return MOE_ERR_INVALID_ARG;
+    if (!seq_ok(s, S)) return s->T < 0 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED;
+    if (!loss || !counts || !slope || (s->T > 0 && (!logits || !topk_idx))) return MOE_ERR_INVALID_ARG;
+    const size_t elem = o.dtype == MOE_DTYPE_F32 ? 4 : 2;
+    if (!aligned(logits, elem) || !aligned(topk_idx, 8) || !aligned(seq_offsets, 4) || !aligned(loss, 4) ||
+        !aligned(counts, 4) || !aligned(slope, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < balance_layout(s, S, nullptr, nullptr))
+        return MOE_ERR_WORKSPACE;
+    if (!device_ok()) return MOE_ERR_DEVICE;
+    BalanceWs ws;
+    balance_layout(s, S, static_cast<uint8_t*>(workspace), &ws);
+    const int64_t chunks = ((int64_t)s->T + kChunk - 1) / kChunk;
+    const unsigned blocks = (unsigned)(chunks > 0 ? chunks : 1);
+    if (o.dtype == MOE_DTYPE_F32)
+        launch_balance_part<MOE_DTYPE_F32>(s, o.score, logits, token_mask, topk_idx, seq_offsets, S, ws, blocks, stream);
+    else
+        launch_balance_part<MOE_DTYPE_BF16>(s, o.score, logits, token_mask, topk_idx, seq_offsets, S, ws, blocks, stream);
+    const int64_t items = (int64_t)S * ((s->E + kFinalExperts - 1) / kFinalExperts);
+    int lanes = 1;
+    while (lanes < kWave && (int64_t)lanes * S < chunks) lanes <<= 1;
+    hipLaunchKernelGGL(k_balance_final, dim3((unsigned)(items < kFinalBlocks ? items : kFinalBlocks)),
+                       dim3(kFinalThreads), 0, stream, s->T, s->E, seq_offsets, S, coef, loss, counts, slope, ws, lanes);
+    return launch_status();
+}
+
+int moe_gate_backward(const moe_gate_shape_t* s, const moe_gate_options_t* opt, const void* logits,
+                      const uint8_t* token_mask, const int64_t* topk_idx, const float* d_topk_w,
+                      const moe_balance_grad_t* balance, void* dlogits, moe_stream_t stream) {
+    const moe_gate_options_t o = opt ? *opt : moe_default_gate_options();
+    moe_balance_grad_t b = {nullptr, nullptr, nullptr, 1};
+    if (balance) b = *balance;
+    if (!s || check_options(&o) != MOE_OK) return MOE_ERR_INVALID_ARG;
+    if (!gate_shape_ok(s)) return s->T < 0 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED;
+    if (balance && (b.S < 1 || (!b.seq_offsets && b.S != 1))) return MOE_ERR_INVALID_ARG;
+    if (balance && !seq_ok(s, b.S)) return MOE_ERR_UNSUPPORTED;
+    if (balance && (!b.slope || !b.d_loss)) return MOE_ERR_INVALID_ARG;
+    if (!topk_idx != !d_topk_w && s->T > 0) return MOE_ERR_INVALID_ARG;
+    if (!topk_idx && !balance && s->T > 0) return MOE_ERR_INVALID_ARG;
+    if (s->T == 0) return MOE_OK;
+    if (!logits || !dlogits) return MOE_ERR_INVALID_ARG;
+    const size_t elem = o.dtype == MOE_DTYPE_F32 ? 4 : 2;
+    if (!aligned(logits, elem) || !aligned(dlogits, elem) || !aligned(topk_idx, 8) || !aligned(d_topk_w, 4) ||
+        !aligned(b.slope, 4) || !aligned(b.d_loss, 4) || !aligned(b.seq_offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_DEVICE;
+    if (o.dtype == MOE_DTYPE_F32)
+        launch_gate_backward<MOE_DTYPE_F32>(s, o, logits, token_mask, topk_idx, d_topk_w, b, dlogits, stream);
+    else
+        launch_gate_backward<MOE_DTYPE_BF16>(s, o, logits, token_mask, topk_idx, d_topk_w, b, dlogits, stream);
+    return launch_status();
+}
+
+}  // extern "C"

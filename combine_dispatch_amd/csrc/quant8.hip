@@ -1,0 +1,405 @@
+// quant8.hip -- quantisers to e4m3 with a scale per block of 128
+// (include/moe_block8.h): rows (1 x 128), weights (128 x 128, with the
+// transposed codes) and columns (128 rows of a column, transposed, groups
+// padded to 128 rows).
+//
+// All three are bound by HBM: 2 or 4 bytes read and 1 (weights with transpose:
+// 2) written per value.  A block's largest |x| is found on the sign-less bit
+// patterns as unsigned integers, where an infinity or NaN is larger than any
+// finite value, so a bad block shows in its scale.
+#include "../../include/moe_block8.h"
+#include "moe_device.hpp"
+#include "moe_host.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kLanes = 16;              // lanes of one 128-wide block, 8 values each
+constexpr int kGroups = kThreads / kLanes;
+constexpr float kMinScale = 0x1p-126f;  // the reciprocal stays finite
+
+template <int N>
+__device__ __forceinline__ uint32_t ror(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x120 + N, 0xF, 0xF, false);
+}
+__device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+    v = umax2(v, ror<8>(v));
+    v = umax2(v, ror<4>(v));
+    v = umax2(v, ror<2>(v));
+    return umax2(v, ror<1>(v));
+}
+
+// 8 values from p[0..n): float32 bit patterns, 0 past n.  VEC: p is 16-byte
+// aligned and n is 8 or nothing.
+template <int DT, bool VEC>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int n, uint32_t (&v)[8]) {
+    if (n <= 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0;
+        return;
+    }
+    if (DT == MOE_DTYPE_F32) {
+        const uint32_t* p = static_cast<const uint32_t*>(base) + at;
+        if (VEC) {
+            const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0u;
+        }
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+        if (VEC) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = w[i] << 16;
+                v[2 * i + 1] = w[i] & 0xFFFF0000u;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? (uint32_t)p[i] << 16 : 0u;
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t abs_max(const uint32_t (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = umax2(m, v[i] & 0x7FFFFFFFu);
+    return m;
+}
+
+// max(amax / 448, 2^-126); fmaxf would drop a NaN.
+__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
+    const float s = __uint_as_float(amax_bits) / 448.f;
+    return s < kMinScale ? kMinScale : s;
+}
+
+// Four values -> four e4m3 bytes, round to nearest even (v_cvt_pk_fp8_f32).
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+__device__ __forceinline__ uint2 pack8(const uint32_t (&v)[8], float inv) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i]) * inv;
+    return make_uint2(pack4(f[0], f[1], f[2], f[3]), pack4(f[4], f[5], f[6], f[7]));
+}
+
+// ---- rows --------------------------------------------------------------------
+// A workgroup takes 32 rows x 512 columns, 16 lanes per (row, block of 128),
+// eight blocks per lane group, all loads first.  The scales go through LDS so
+// that each k-block's 32 scales leave as one 128-byte run.
+constexpr int kRowTile = 32, kColBlocks = 4;
+
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kThreads) void k_quantise_rows(const void* __restrict__ x, int64_t R, int C, int kb,
+                                                            const int32_t* __restrict__ rows_used,
+                                                            uint8_t* __restrict__ codes,
+                                                            float* __restrict__ scales) {
+    __shared__ float lds_s[kColBlocks][kRowTile];
+    const int j = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+    const int64_t r0 = (int64_t)blockIdx.x * kRowTile;
+    const int kb0 = blockIdx.y * kColBlocks;
+    int64_t used = R;
+    if (rows_used) {
+        const int64_t n = *rows_used;
+        used = n < 0 ? 0 : (n < R ? n : R);
+    }
+    if (r0 >= used) return;
+    constexpr int kPer = kRowTile * kColBlocks / kGroups;
+    uint32_t v[kPer][8];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {  // block i of this lane group: k-block i % 4, row grp + 16 (i / 4)
+        const int b = kb0 + i % kColBlocks;
+        const int64_t r = r0 + grp + kGroups * (i / kColBlocks);
+        const int c = b * 128 + j * 8;
+        load8<DT, VEC>(x, r * C + c, r < used ? (C - c < 8 ? C - c : 8) : 0, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int b = kb0 + i % kColBlocks, rl = grp + kGroups * (i / kColBlocks);
+        const int64_t r = r0 + rl;
+        const float s = block_scale(row_max(abs_max(v[i])));
+        if (j == 0) lds_s[i % kColBlocks][rl] = s;
+        if (r < used && b < kb)
+            *reinterpret_cast<uint2*>(codes + r * ((int64_t)kb * 128) + b * 128 + j * 8) = pack8(v[i], 1.f / s);
+    }
+    __syncthreads();
+    if (threadIdx.x < kRowTile * kColBlocks) {
+        const int b = threadIdx.x / kRowTile, rl = threadIdx.x % kRowTile;
+        if (kb0 + b < kb && r0 + rl < used) scales[(int64_t)(kb0 + b) * R + r0 + rl] = lds_s[b][rl];
+    }
+}
+
+// ---- weights -----------------------------------------------------------------
+// One 128 x 128 block per workgroup: 16 lanes per row, eight rows per lane
+// group, held in registers while the block's largest value is found.  The
+// transposed codes go through a 16 KiB LDS tile of 4 x 4 byte blocks: a lane
+// writes the words of its columns, then reads rows of the transpose.
+__device__ __forceinline__ int t_word(int col, int word) {  // word = row / 4 of transposed row col
+    return col * 32 + ((word + col / 8 * 2) & 31);
+}
+
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kThreads) void k_quantise_weights(const void* __restrict__ w, int N, int K,
+                                                               uint8_t* __restrict__ codes,
+                                                               float* __restrict__ scales,
+                                                               uint8_t* __restrict__ codes_t,
+                                                               float* __restrict__ scales_t) {
+    __shared__ uint32_t lds_m[kThreads / kWave];
+    __shared__ uint32_t lds_t[128 * 32];
+    const int j = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+    const int kb = (K + 127) / 128, nb = (N + 127) / 128;
+    const int k0 = blockIdx.x * 128, n0 = blockIdx.y * 128;
+    const int64_t e = blockIdx.z;
+    const int c = k0 + j * 8;
+    uint32_t v[8][8], m = 0;
+    // rows 8 grp .. 8 grp + 7, so that a lane holds whole 4-byte words of the transpose
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int n = n0 + grp * 8 + i;
+        load8<DT, VEC>(w, (e * N + n) * (int64_t)K + c, n < N ? (K - c < 8 ? K - c : 8) : 0, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = umax2(m, abs_max(v[i]));
+    for (int x = 1; x < kWave; x <<= 1) m = umax2(m, (uint32_t)__shfl_xor((int)m, x));
+    if (threadIdx.x % kWave == 0) lds_m[threadIdx.x / kWave] = m;
+    __syncthreads();
+    m = umax2(umax2(lds_m[0], lds_m[1]), umax2(lds_m[2], lds_m[3]));
+    const float s = block_scale(m), inv = 1.f / s;
+    uint2 q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int n = n0 + grp * 8 + i;
+        q[i] = pack8(v[i], inv);
+        if (n < N) *reinterpret_cast<uint2*>(codes + (e * N + n) * ((int64_t)kb * 128) + c) = q[i];
+    }
+    if (threadIdx.x == 0) scales[(e * nb + blockIdx.y) * kb + blockIdx.x] = s;
+    if (!codes_t) return;
+    if (threadIdx.x == 0) scales_t[(e * kb + blockIdx.x) * nb + blockIdx.y] = s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // column c + i: rows 0-3 and 4-7 of this lane, one word each
+        const int sh = 8 * (i % 4);
+        uint32_t a = 0, b = 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            a |= (((i < 4 ? q[r].x : q[r].y) >> sh) & 0xFFu) << (8 * r);
+            b |= (((i < 4 ? q[r + 4].x : q[r + 4].y) >> sh) & 0xFFu) << (8 * r);
+        }
+        lds_t[t_word(j * 8 + i, 2 * grp)] = a;
+        lds_t[t_word(j * 8 + i, 2 * grp + 1)] = b;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // transposed row grp + 16 i, bytes 8 j ..
+        const int col = grp + kGroups * i, k = k0 + col;
+        const uint2 o = make_uint2(lds_t[t_word(col, 2 * j)], lds_t[t_word(col, 2 * j + 1)]);
+        if (k < K) *reinterpret_cast<uint2*>(codes_t + (e * K + k) * ((int64_t)nb * 128) + n0 + j * 8) = o;
+    }
+}
+
+// ---- columns -------------------------------------------------------------------
+// One block of 128 padded rows x 128 columns per workgroup.  The workgroup
+// finds its group by adding up the groups' padded sizes (each thread a few
+// experts, an integer scan).  Thread layout as for the weights; the columns'
+// largest values meet in LDS.
+constexpr int kMaxGroups = 1024;
+
+__device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+// The smallest power of two s >= 2^-126 with amax <= 448 s, as its UE8M0 byte
+// (255 for an infinity or NaN), and 1 / s.
+__device__ __forceinline__ uint32_t pow2_scale(uint32_t amax_bits, float& inv) {
+    if (amax_bits >= 0x7F800000u) {
+        inv = __uint_as_float(0x7FC00000u);
+        return 255u;
+    }
+    const int b = clamp_int((int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0), 1, 254);
+    inv = __uint_as_float((uint32_t)(254 - b) << 23);  // b <= 247 for finite amax
+    return (uint32_t)b;
+}
+
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kThreads) void k_quantise_columns(const void* __restrict__ x, int64_t R, int C, int E,
+                                                               const int32_t* __restrict__ offsets, int64_t Rp,
+                                                               uint8_t* __restrict__ codes,
+                                                               uint8_t* __restrict__ scales) {
+    __shared__ uint32_t lds_m[kGroups][128];
+    __shared__ uint32_t lds_t[128 * 32];
+    __shared__ int lds_wave[kThreads / kWave];
+    __shared__ int lds_at[2];
+    const int tid = threadIdx.x, j = tid % kLanes, grp = tid / kLanes;
+    const int64_t pb = blockIdx.x;  // padded row block
+    int64_t lo = pb * 128, hi = R;
+    if (offsets) {
+        // blocks of experts 4 tid .. 4 tid + 3
+        constexpr int kPer = kMaxGroups / kThreads;
+        int first[kPer], n[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = tid * kPer + i;
+            first[i] = 0;
+            n[i] = 0;
+            if (e < E) {
+                first[i] = clamp_int(offsets[e], 0, (int)R);
+                n[i] = clamp_int(offsets[e + 1], first[i], (int)R) - first[i];
+            }
+            sum += (n[i] + 127) / 128;
+        }
+        int before = sum;
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int up = __shfl_up(before, d);
+            before += tid % kWave >= d ? up : 0;
+        }
+        if (tid % kWave == kWave - 1) lds_wave[tid / kWave] = before;
+        if (tid == 0) lds_at[0] = -1;
+        __syncthreads();
+        before -= sum;
+        for (int wv = 0; wv < tid / kWave; ++wv) before += lds_wave[wv];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int nb = (n[i] + 127) / 128;
+            if (pb >= before && pb < before + nb) {
+                lds_at[0] = first[i] + (int)(pb - before) * 128;
+                lds_at[1] = first[i] + n[i];
+            }
+            before += nb;
+        }
+        __syncthreads();
+        if (lds_at[0] < 0) return;  // behind the last group's blocks
+        lo = lds_at[0];
+        hi = lds_at[1];
+    }
+    const int c0 = blockIdx.y * 128, c = c0 + j * 8;
+    uint32_t v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = lo + grp * 8 + i;
+        load8<DT, VEC>(x, r * C + c, r < hi ? (C - c < 8 ? C - c : 8) : 0, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) m = umax2(m, v[r][i] & 0x7FFFFFFFu);
+        lds_m[grp][j * 8 + i] = m;
+    }
+    __syncthreads();
+    if (tid < 128) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) m = umax2(m, lds_m[g][tid]);
+        float inv;
+        const uint32_t b = pow2_scale(m, inv);
+        lds_m[0][tid] = __float_as_uint(inv);
+        if (c0 + tid < C) scales[pb * C + c0 + tid] = (uint8_t)b;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // column c + i
+        const float inv = __uint_as_float(lds_m[0][j * 8 + i]);
+        float f[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) f[r] = __uint_as_float(v[r][i]) * inv;
+        lds_t[t_word(j * 8 + i, 2 * grp)] = pack4(f[0], f[1], f[2], f[3]);
+        lds_t[t_word(j * 8 + i, 2 * grp + 1)] = pack4(f[4], f[5], f[6], f[7]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int col = grp + kGroups * i;
+        const uint2 o = make_uint2(lds_t[t_word(col, 2 * j)], lds_t[t_word(col, 2 * j + 1)]);
+        if (c0 + col < C) *reinterpret_cast<uint2*>(codes + (int64_t)(c0 + col) * Rp + pb * 128 + j * 8) = o;
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------
+constexpr int32_t kMaxDim = 1 << 20;
+constexpr int64_t kMaxRows = int64_t(1) << 28;  // a launch holds fewer than 2^32 threads
+
+bool dtype_ok(int dt) { return dt == MOE_DTYPE_F32 || dt == MOE_DTYPE_BF16; }
+bool elem_aligned(const void* p, int dt) { return aligned(p, dt == MOE_DTYPE_F32 ? 4 : 2); }
+// whole 8-value vectors on 16-byte boundaries in every row
+bool vectors(const void* p, int cols) { return aligned(p, 16) && cols % 8 == 0; }
+
+// f(dtype, vectors) as compile-time constants
+template <typename F>
+void with_input(int dt, bool vec, F f) {
+    using std::integral_constant;
+    if (dt == MOE_DTYPE_F32 && vec) f(integral_constant<int, MOE_DTYPE_F32>(), integral_constant<bool, true>());
+    else if (dt == MOE_DTYPE_F32) f(integral_constant<int, MOE_DTYPE_F32>(), integral_constant<bool, false>());
+    else if (vec) f(integral_constant<int, MOE_DTYPE_BF16>(), integral_constant<bool, true>());
+    else f(integral_constant<int, MOE_DTYPE_BF16>(), integral_constant<bool, false>());
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int64_t moe_padded_rows(int64_t R, int32_t E) {
+    if (R < 0 || R > kMaxRows || E < 1 || E > kMaxGroups) return 0;
+    return (R + 127 * (int64_t)E) / 128 * 128;
+}
+
+int moe_quantise_rows(int64_t R, int32_t C, int32_t dtype, const void* x, const int32_t* rows_used, uint8_t* codes,
+                      float* scales, moe_stream_t stream) {
+    if (R < 0 || C < 1 || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    if (R > kMaxRows || C > kMaxDim) return MOE_ERR_UNSUPPORTED;
+    if (R == 0) return MOE_OK;
+    if (!x || !codes || !scales) return MOE_ERR_INVALID_ARG;
+    if (!elem_aligned(x, dtype) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(rows_used, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_DEVICE;
+    const int kb = (C + 127) / 128;
+    const dim3 grid((unsigned)((R + kRowTile - 1) / kRowTile), (unsigned)((kb + kColBlocks - 1) / kColBlocks));
+    with_input(dtype, vectors(x, C), [&](auto dt, auto vec) {
+        hipLaunchKernelGGL((k_quantise_rows<decltype(dt)::value, decltype(vec)::value>), grid, dim3(kThreads), 0,
+                           stream, x, R, C, kb, rows_used, codes, scales);
+    });
+    return launch_status();
+}
+
+int moe_quantise_weights(int32_t E, int32_t N, int32_t K, int32_t dtype, const void* w, uint8_t* codes, float* scales,
+                         uint8_t* codes_t, float* scales_t, moe_stream_t stream) {
+    if (E < 1 || N < 1 || K < 1 || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    if (E > 65535 || N > kMaxDim || K > kMaxDim) return MOE_ERR_UNSUPPORTED;
+    if (!w || !codes || !scales || !codes_t != !scales_t) return MOE_ERR_INVALID_ARG;
+    if (!elem_aligned(w, dtype) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(codes_t, 16) ||
+        !aligned(scales_t, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_DEVICE;
+    const dim3 grid((unsigned)((K + 127) / 128), (unsigned)((N + 127) / 128), (unsigned)E);
+    with_input(dtype, vectors(w, K), [&](auto dt, auto vec) {
+        hipLaunchKernelGGL((k_quantise_weights<decltype(dt)::value, decltype(vec)::value>), grid, dim3(kThreads), 0,
+                           stream, w, N, K, codes, scales, codes_t, scales_t);
+    });
+    return launch_status();
+}
+
+int moe_quantise_columns(int64_t R, int32_t C, int32_t E, int32_t dtype, const void* x, const int32_t* offsets,
+                         uint8_t* codes, uint8_t* scales, moe_stream_t stream) {
+    if (R < 0 || C < 1 || E < 1 || !dtype_ok(dtype) || (!offsets && E != 1)) return MOE_ERR_INVALID_ARG;
+    if (R > kMaxRows || C > kMaxDim || E > kMaxGroups) return MOE_ERR_UNSUPPORTED;
+    const int64_t Rp = moe_padded_rows(R, E);
+    if (R == 0) return MOE_OK;
+    if (!x || !codes || !scales) return MOE_ERR_INVALID_ARG;
+    if (!elem_aligned(x, dtype) || !aligned(codes, 16) || !aligned(offsets, 4)) return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_DEVICE;
+    const dim3 grid((unsigned)(Rp / 128), (unsigned)((C + 127) / 128));
+    with_input(dtype, vectors(x, C), [&](auto dt, auto vec) {
+        hipLaunchKernelGGL((k_quantise_columns<decltype(dt)::value, decltype(vec)::value>), grid, dim3(kThreads), 0,
+                           stream, x, R, C, E, offsets, Rp, codes, scales);
+    });
+    return launch_status();
+}
+
+}  // extern "C"

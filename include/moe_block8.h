@@ -1,0 +1,102 @@
+/*
+ * moe_block8.h -- matrix products in FP8 e4m3 with one scale per block of 128,
+ * grouped over the experts of a pool (one group = a dense product), their
+ * gradients, and the quantisers that make their operands.
+ *
+ * The pool is the expert-major one of moe_dispatch (bf16 payload): rows
+ * offsets[e] .. offsets[e+1] - 1 belong to expert e.  Conventions as in moe.h:
+ * device pointers, row-major, densely packed, caller-owned buffers,
+ * asynchronous on `stream`, MOE_OK or a negative status, nothing allocated,
+ * nothing synchronised, capturable into a HIP graph, results independent of
+ * timing.  No call needs a workspace.
+ *
+ * Layouts (C' = C rounded up to a multiple of 128; codes past C are 0):
+ *   rows     codes [R][C'], scales fp32 [C'/128][R]: value = code * scales[c/128][r]
+ *   weights  codes [E][N][K'], scales fp32 [E][N'/128][K'/128]:
+ *            value = code * scales[e][n/128][k/128]
+ *   columns  codes [C][R'] (transposed; each group's rows start at a multiple
+ *            of 128 and are padded with 0 to one), scales UE8M0 bytes
+ *            [R'/128][C]: value = code * 2^(scales[r'/128][c] - 127)
+ * fp32 scales are max(amax / 448, 2^-126) of the block and a code is
+ * e4m3(x * (1 / scale)), round to nearest even; column scales are the smallest
+ * power of two s >= 2^-126 with amax <= 448 s.  A block that holds an infinity
+ * or NaN gets a scale that is not finite (fp32) or the UE8M0 NaN byte 255, so
+ * that its products are NaN.
+ */
+#ifndef MOE_BLOCK8_H
+#define MOE_BLOCK8_H
+
+#include "moe_gate.h" /* MOE_DTYPE_* */
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Rows of the columns layout: R' for R rows in E groups, (R + 127 E) / 128 * 128
+ * (whole number; every division of R rows into E groups fits). 0 on bad arguments. */
+int64_t moe_padded_rows(int64_t R, int32_t E);
+
+/*
+ * x [R][C] of dtype -> rows layout.  rows_used: device int32 [1] or NULL; rows
+ * at or past *rows_used are left as they are (pass offsets + E for a pool of
+ * larger capacity).  0 <= R <= 2^28, 1 <= C <= 2^20.
+ */
+int moe_quantise_rows(int64_t R, int32_t C, int32_t dtype, const void* x, const int32_t* rows_used,
+                      uint8_t* codes, float* scales, moe_stream_t stream);
+
+/*
+ * w [E][N][K] of dtype -> weights layout; with codes_t and scales_t (both or
+ * neither NULL) also that of the transposed weights [E][K][N], the same values:
+ * codes_t [E][K][N'], scales_t [E][K'/128][N'/128].  1 <= E <= 65535, 1 <= N, K <= 2^20.
+ */
+int moe_quantise_weights(int32_t E, int32_t N, int32_t K, int32_t dtype, const void* w,
+                         uint8_t* codes, float* scales, uint8_t* codes_t, float* scales_t,
+                         moe_stream_t stream);
+
+/*
+ * x [R][C] of dtype -> columns layout, R' = moe_padded_rows(R, E) rows long.
+ * offsets int32 [E+1] or NULL (E must be 1: one group of all R rows).  Padded
+ * rows past the last group's are left as they are.
+ * 0 <= R <= 2^28, 1 <= C <= 2^20, 1 <= E <= 1024.
+ */
+int moe_quantise_columns(int64_t R, int32_t C, int32_t E, int32_t dtype, const void* x,
+                         const int32_t* offsets, uint8_t* codes, uint8_t* scales,
+                         moe_stream_t stream);
+
+typedef struct {
+    int64_t R; /* rows (of the pool, or of a dense product), 0..2^28 (wgrad: 0..2^23) */
+    int32_t N; /* output features, 1..2^20 */
+    int32_t K; /* input features, a multiple of 128, up to 2^20 */
+    int32_t E; /* groups, 1..1024 */
+} moe_block_shape_t;
+
+/*
+ * out bf16 [R][N]: out[r][n] = sum over k of a[r][k] w[e(r)][n][k], a in rows
+ * layout with C' = K, w in weights layout with K' = K, 16-byte aligned codes.
+ * Each 128-wide block is a matrix-core sum, scaled and added in float32; the
+ * result is rounded to bf16 once.  Rows outside offsets[0] .. offsets[E] - 1
+ * are left as they are.  offsets NULL: E must be 1, all R rows.  Offsets out
+ * of order or range give some result but no access out of bounds.
+ * The gradient by the input is the same product: a = the quantised gradient,
+ * w = the transposed weights (codes_t, scales_t), K and N exchanged.
+ */
+int moe_block_gemm(const moe_block_shape_t* s, const uint8_t* a, const float* a_scales,
+                   const uint8_t* w, const float* w_scales, const int32_t* offsets, void* out,
+                   moe_stream_t stream);
+
+/*
+ * The gradient by the weights: out bf16 [E][N][K], out[e][n][k] = sum over the
+ * rows r of group e of g[r][n] x[r][k]; g (the output's gradient, N columns)
+ * and x (the input, K columns) in columns layout over the same offsets, codes
+ * 16-byte aligned.  Here K need not be a multiple of 128.  A group without
+ * rows gets zeros.  The power-of-two scales are applied inside the matrix
+ * cores, which sum in float32.
+ */
+int moe_block_gemm_wgrad(const moe_block_shape_t* s, const uint8_t* g, const uint8_t* g_scales,
+                         const uint8_t* x, const uint8_t* x_scales, const int32_t* offsets,
+                         void* out, moe_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif

@@ -1,0 +1,119 @@
+/*
+ * moe_gate.h -- the router in front of the MoE layer: top-k gate with its
+ * gradient, balance loss with per-expert counts and its gradient.
+ *
+ * moe_gate writes the topk_idx / topk_w that moe_dispatch and the fused layer
+ * read.  Conventions as in moe.h: device pointers, row-major, densely packed,
+ * caller-owned buffers, asynchronous on `stream`, MOE_OK or a negative status,
+ * nothing allocated, nothing synchronised, T == 0 launches nothing (but see
+ * moe_balance_loss).  Calls may be captured into a HIP graph.  All sums, softmax statistics
+ * and gradients are float32 or wider; outputs in bf16 are rounded once.
+ * Results do not depend on timing: no floating-point atomics on global memory.
+ *
+ * Masks.  token_mask (uint8 [T], NULL = all tokens live): a token with 0 is
+ * padding; it gets topk_idx -1 and topk_w 0, counts nowhere and has a zero
+ * gradient row, whatever its logits hold.  A logit of -inf takes that expert
+ * out for that token; slots that find no expert get -1 and 0.  The type's
+ * lowest finite value is an ordinary logit.  NaN sorts above everything (and
+ * so reaches topk_w), as in torch.topk.
+ */
+#ifndef MOE_GATE_H
+#define MOE_GATE_H
+
+#include "moe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1 };
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+typedef struct {
+    int32_t T; /* tokens, 0..2^27 */
+    int32_t E; /* experts, 1..1024 */
+    int32_t K; /* slots per token, 1..min(E, 64) */
+} moe_gate_shape_t;
+
+typedef struct {
+    int32_t dtype;       /* of logits and dlogits: MOE_DTYPE_F32 or MOE_DTYPE_BF16 */
+    int32_t score;       /* s = softmax(logits) over the E experts, or 1 / (1 + exp(-logits)) */
+    int32_t renormalise; /* 1: the K weights of a token sum to `scale`; 0: w = scale * s */
+    float scale;         /* finite */
+} moe_gate_options_t;
+
+/* f32 logits, softmax, renormalised, scale 1. */
+moe_gate_options_t moe_default_gate_options(void);
+
+/*
+ * Per token the K experts of the largest key, in descending order, equal keys
+ * by the lower index:
+ *   key_e = logit_e                      (softmax, or sigmoid without a bias)
+ *   key_e = sigmoid(logit_e) + bias_e    (sigmoid with a bias; compared as
+ *                                         float64 wherever float32 could err)
+ *   topk_w = scale * s_e / sum of the chosen s   (renormalise; 0 where that sum is 0)
+ *          = scale * s_e                         (otherwise)
+ * The bias steers the choice only; the weights come from s.
+ *   logits   [T][E] of opt->dtype
+ *   bias     fp32 [E] or NULL; with MOE_SCORE_SOFTMAX it must be NULL
+ *   topk_idx int64 [T][K], topk_w fp32 [T][K]
+ */
+int moe_gate(const moe_gate_shape_t* s, const moe_gate_options_t* opt /* NULL = defaults */,
+             const void* logits, const float* bias, const uint8_t* token_mask, int64_t* topk_idx,
+             float* topk_w, moe_stream_t stream);
+
+/*
+ * Balance loss over S sequences of the batch (sequence q holds the tokens
+ * seq_offsets[q] .. seq_offsets[q+1] - 1; seq_offsets int32 [S+1], ascending;
+ * NULL: one sequence of all T tokens, S must be 1).  With n_q live tokens,
+ * c_qe slots of sequence q that name expert e, P_qe the mean over its live
+ * tokens of p_te = s_te / sum_e s_te, and Q the number of sequences with
+ * n_q > 0:
+ *   loss = coef / Q * sum over q, e of (E * c_qe / sum_e c_qe) * P_qe
+ * (a sequence without live tokens or without counted slots adds 0).
+ *   topk_idx int64 [T][K]; negative or >= E: not counted; the slots of a
+ *            padding token are not counted
+ *   loss     fp32 [1]
+ *   counts   int32 [S][E]: c_qe
+ *   slope    fp32 [S][E]: d loss / d p_te of a live token of sequence q, the
+ *            counts taken as constants; moe_gate_backward reads it
+ *   workspace: moe_balance_workspace_bytes(s, S) bytes, 16-byte aligned;
+ *            contents on entry do not matter.  Calls that overlap in time need
+ *            one each (two captured graphs that may run at once too).
+ * T == 0 writes zeros to loss, counts and slope.  1 <= S <= 65536; S * E < 2^31.
+ * Offsets out of order or out of 0..T give some result but no access out of
+ * bounds.
+ */
+size_t moe_balance_workspace_bytes(const moe_gate_shape_t* s, int32_t S);
+int moe_balance_loss(const moe_gate_shape_t* s, const moe_gate_options_t* opt, const void* logits,
+                     const uint8_t* token_mask, const int64_t* topk_idx, const int32_t* seq_offsets,
+                     int32_t S, float coef, float* loss, int32_t* counts, float* slope,
+                     void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* The balance loss' part of the gradient: slope and seq_offsets as above,
+ * d_loss fp32 [1] on the device. */
+typedef struct {
+    const float* slope;
+    const float* d_loss;
+    const int32_t* seq_offsets; /* NULL: one sequence */
+    int32_t S;
+} moe_balance_grad_t;
+
+/*
+ * dlogits [T][E] (fully overwritten) = the gradient through topk_w, the choice
+ * held fixed, plus the gradient through the balance loss; in one pass, either
+ * part may be left out.
+ *   topk_idx, d_topk_w: int64 / fp32 [T][K], both NULL = no gate part;
+ *            topk_idx as moe_gate wrote it (an expert at most once per token;
+ *            negative or >= E: the slot has no gradient)
+ *   balance  NULL = no balance part
+ * The logits have to be those of the forward call (scores are recomputed).
+ */
+int moe_gate_backward(const moe_gate_shape_t* s, const moe_gate_options_t* opt, const void* logits,
+                      const uint8_t* token_mask, const int64_t* topk_idx, const float* d_topk_w,
+                      const moe_balance_grad_t* balance, void* dlogits, moe_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif
