@@ -18,9 +18,10 @@
 //
 // Layout.  P and Q tiles of one K step go straight from global memory to LDS
 // (128-byte rows; 16-byte chunks XOR-swizzled through the load's source
-// address so that each 16 lanes of a ds_read_b128 meet distinct banks).  The
-// MFMA's row r of column tile j is LDS row (r / 4) * 4J + 4j + r % 4 of the
-// wave's Q rows, so that a lane ends up with 4J adjacent outputs of a row.
+// address so that each 16 lanes of a ds_read_b128 meet distinct banks).  LDS
+// row 32 j + r of a wave's Q rows, the MFMA's row r of tile j, is row
+// (r / 4) * 4J + 4j + r % 4 of them, so that a lane ends up with 4J adjacent
+// outputs of a row.
 // The k order inside a 64-wide MFMA is the same permutation for both operands.
 #include "../../include/moe_block8.h"
 #include "moe_device.hpp"
@@ -58,12 +59,18 @@ __device__ __forceinline__ void dma_x1(uint32_t lds, const void* sbase, uint32_t
                  "v"(voff), "s"(uniform_ptr(sbase))
                  : "memory");
 }
-// All of this wave's loads but the newest N have landed and its LDS reads are
-// done; then the workgroup meets.
+// All of this wave's loads but the newest N have landed (and its LDS reads are
+// done; then the workgroup meets).  Stores count as loads do.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
+__device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
 
 __device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
@@ -91,16 +98,6 @@ __device__ __forceinline__ void group_rows(const BlockArgs& g, int e, int& lo, i
     n = clamp_int(g.offsets[e + 1], lo, (int)g.R) - lo;
 }
 
-// One output tile: operand bases (uniform), valid rows and columns, K steps.
-struct Tile {
-    const uint8_t* p;
-    const uint8_t* q;
-    const uint8_t* ps;
-    const uint8_t* qs;
-    uint16_t* out;
-    int rows, cols, nk;
-};
-
 template <int MODE_, int WQ_, int WP_, int J_, int TT_, int STAGES_, int GROUP_, int PER_CU_>
 struct Cfg {
     static constexpr int MODE = MODE_, WQ = WQ_, WP = WP_, J = J_, TT = TT_, STAGES = STAGES_, GROUP = GROUP_,
@@ -108,176 +105,345 @@ struct Cfg {
     static constexpr int BQ = 32 * J * WQ, BP = 32 * TT * WP, WAVES = WQ * WP, THREADS = 64 * WAVES;
     static constexpr int PP = BP * 8 / THREADS, QP = BQ * 8 / THREADS;  // 16-byte loads per thread and step
     static constexpr int ROWS = THREADS / 8;                            // LDS rows one pass fills
-    static constexpr int LOADS = PP + QP + (MODE == kProduct ? 1 : 0);  // per wave and step
+    static constexpr int LOADS = PP + QP + 1;                           // per wave and step
     static constexpr int QOFF = BP * kBK, SOFF = (BP + BQ) * kBK;
-    static constexpr int STAGE = SOFF + (MODE == kProduct ? BP * 4 + 256 : 0);
-    static_assert(BP / 64 < WAVES || MODE == kWgrad, "a wave for the Q scales");
-    static_assert(ROWS % 16 == 0 && ROWS % (16 * J) == 0, "a thread's chunk does not depend on the pass");
+    static constexpr int TABLE_PRE = kMaxGroups + 4, TABLE_REC = THREADS * (MODE == kProduct ? 4 : 5);
+    static constexpr int TABLE = TABLE_PRE > TABLE_REC ? TABLE_PRE : TABLE_REC;
+    static constexpr int STAGE = SOFF + (MODE == kProduct ? BP * 4 + 256 : WAVES * 256);
+    static_assert(MODE == kProduct ? BP / 64 < WAVES : BP / 64 + BQ / 64 == WAVES, "a wave for every 64 scales");
+    static_assert(ROWS % 16 == 0, "a thread's chunk does not depend on the pass");
 };
 
-// Swizzle keys of LDS rows: 16-byte chunk c of row r lies at chunk c ^ key(r).
-__device__ __forceinline__ int p_key(int r) { return (r >> 1) & 7; }
+// 16-byte chunk c of LDS row r lies at chunk c ^ row_key(r).
+__device__ __forceinline__ int row_key(int r) { return (r >> 1) & 7; }
+// The Q row that LDS row r holds.
 template <int J>
-__device__ __forceinline__ int q_key(int r) {
-    return ((r / (4 * J)) & 3) << 1 | ((r >> 1) & 1);
+__device__ __forceinline__ int q_row(int r) {
+    return r / (32 * J) * (32 * J) + (r % 32 / 4) * (4 * J) + r / 32 % J * 4 + r % 4;
 }
 
-template <class C>
-struct Worker {
-    static constexpr int MODE = C::MODE;
-    const BlockArgs& g;
-    uint8_t* lds;
-    const int* pre;  // product: m-tiles before expert e; wgrad: K steps before group e
-    int tid, lane, wave, wq, wp;
-    int nq, np;  // tiles along q; along p (wgrad)
+// A workgroup's tiles, worked out by all its threads at the start and kept in
+// LDS: x = first row of P (product: of the pool; wgrad: of the gradient's
+// columns), y = valid rows (product) or the group's first K step (wgrad),
+// z = group, w = tile along q; k = K steps.
+struct TileRec {
+    int x, y, z, w;
+};
 
-    __device__ __forceinline__ Worker(const BlockArgs& g_, uint8_t* l, const int* t) : g(g_), lds(l), pre(t) {
+// The shape of the tile order, the same for the whole grid.
+template <class C>
+struct Order {
+    int nq, np;  // tiles along q; along p (wgrad)
+    uint32_t total;
+
+    // pre: product: m-tiles before group e; wgrad: K steps before group e
+    __device__ __forceinline__ Order(const BlockArgs& g, const int* pre) {
+        nq = ((C::MODE == kProduct ? g.N : g.K) + C::BQ - 1) / C::BQ;
+        np = (g.N + C::BP - 1) / C::BP;
+        total = (uint32_t)__builtin_amdgcn_readfirstlane((C::MODE == kProduct ? pre[g.E] : g.E * np) * nq);
+    }
+    // Tile idx of the order: GROUP p-tiles by all q-tiles, p fastest.
+    __device__ __forceinline__ TileRec at(const BlockArgs& g, const int* pre, uint32_t idx) const {
+        const uint32_t mt = (uint32_t)(C::MODE == kProduct ? pre[g.E] : g.E * np);
+        const uint32_t span = (uint32_t)C::GROUP * (uint32_t)nq, grp = idx / span, in = idx % span;
+        const uint32_t left = mt - grp * C::GROUP, gm = left < C::GROUP ? left : C::GROUP;
+        const int m = (int)(grp * C::GROUP + in % gm);
+        TileRec t;
+        t.w = (int)(in / gm);
+        if (C::MODE == kProduct) {
+            int lo = 0, hi = g.E;  // the group of m-tile m: pre[lo] <= m < pre[lo + 1]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (pre[mid] <= m) lo = mid;
+                else hi = mid;
+            }
+            int first, n;
+            group_rows(g, lo, first, n);
+            const int r0 = (m - pre[lo]) * C::BP;
+            t.x = first + r0;
+            t.y = n - r0 < C::BP ? n - r0 : C::BP;
+            t.z = lo;
+        } else {
+            t.z = m / np;
+            t.x = m % np * C::BP;
+            t.y = clamp_int(pre[t.z], 0, (int)(g.ld / kBK));
+        }
+        return t;
+    }
+};
+
+// A tile as the waves use it: everything uniform.
+template <class C>
+struct Tile {
+    int x, y, z, w, rows, cols, nk;
+
+    __device__ __forceinline__ void read(const BlockArgs& g, const TileRec* rec, const int* steps, int n) {
+        const TileRec r = rec[n];
+        x = __builtin_amdgcn_readfirstlane(r.x);
+        y = __builtin_amdgcn_readfirstlane(r.y);
+        z = __builtin_amdgcn_readfirstlane(r.z);
+        w = __builtin_amdgcn_readfirstlane(r.w);
+        const int q = C::MODE == kProduct ? g.N : g.K;
+        cols = q - w * C::BQ < C::BQ ? q - w * C::BQ : C::BQ;
+        if (C::MODE == kProduct) {
+            rows = y;
+            nk = g.K / kBK;
+        } else {
+            rows = g.N - x < C::BP ? g.N - x : C::BP;
+            nk = __builtin_amdgcn_readfirstlane(steps[n]);
+        }
+    }
+    __device__ __forceinline__ uint16_t* out(const BlockArgs& g) const {
+        return C::MODE == kProduct ? g.out + (int64_t)x * g.N + w * C::BQ
+                                   : g.out + ((int64_t)z * g.N + x) * g.K + w * C::BQ;
+    }
+};
+
+// Where a wave and its lanes stand.
+template <class C>
+struct Place {
+    int tid, lane, wave, wq, wp;
+    __device__ __forceinline__ Place() {
         tid = threadIdx.x;
         lane = tid & 63;
         wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         wq = wave % C::WQ;
         wp = wave / C::WQ;
-        nq = ((MODE == kProduct ? g.N : g.K) + C::BQ - 1) / C::BQ;
-        np = (g.N + C::BP - 1) / C::BP;
-    }
-    __device__ __forceinline__ int64_t tiles() const {
-        return MODE == kProduct ? (int64_t)pre[g.E] * nq : (int64_t)g.E * np * nq;
-    }
-
-    // Tile idx of the order: GROUP p-tiles by all q-tiles, p fastest.
-    __device__ __forceinline__ Tile at(int64_t idx) const {
-        const int64_t mt = MODE == kProduct ? (int64_t)pre[g.E] : (int64_t)g.E * np;
-        const int64_t grp = idx / ((int64_t)C::GROUP * nq), in = idx % ((int64_t)C::GROUP * nq);
-        const int64_t left = mt - grp * C::GROUP;
-        const int gm = left < C::GROUP ? (int)left : C::GROUP;
-        const int64_t m = grp * C::GROUP + in % gm;
-        const int qt = __builtin_amdgcn_readfirstlane((int)(in / gm));
-        Tile t;
-        if (MODE == kProduct) {
-            int lo = 0, hi = g.E;  // the expert of m-tile m: pre[lo] <= m < pre[lo + 1]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (pre[mid] <= (int)m) lo = mid;
-                else hi = mid;
-            }
-            const int e = __builtin_amdgcn_readfirstlane(lo);
-            int first, n;
-            group_rows(g, e, first, n);
-            const int r0 = ((int)m - pre[e]) * C::BP;
-            const int64_t row = (int64_t)first + r0;
-            const int q0 = qt * C::BQ, kb = g.K / kBK, nb = (g.N + 127) / 128;
-            t.rows = n - r0 < C::BP ? n - r0 : C::BP;
-            t.cols = g.N - q0 < C::BQ ? g.N - q0 : C::BQ;
-            t.nk = kb;
-            t.p = g.p + row * g.ld;
-            t.q = g.q + ((int64_t)e * g.N + q0) * g.ld;
-            t.ps = (const uint8_t*)((const float*)g.ps + row);
-            t.qs = (const uint8_t*)((const float*)g.qs + ((int64_t)e * nb + q0 / 128) * kb);
-            t.out = g.out + row * g.N + q0;
-        } else {
-            const int e = __builtin_amdgcn_readfirstlane((int)(m / np)), p0 = (int)(m % np) * C::BP, q0 = qt * C::BQ;
-            const int most = (int)(g.ld / kBK), k0 = clamp_int(pre[e], 0, most);
-            t.rows = g.N - p0 < C::BP ? g.N - p0 : C::BP;
-            t.cols = g.K - q0 < C::BQ ? g.K - q0 : C::BQ;
-            t.nk = clamp_int(pre[e + 1], k0, most) - k0;
-            t.p = g.p + p0 * g.ld + (int64_t)k0 * kBK;
-            t.q = g.q + q0 * g.ld + (int64_t)k0 * kBK;
-            t.ps = (const uint8_t*)g.ps + (int64_t)k0 * g.N + p0;
-            t.qs = (const uint8_t*)g.qs + (int64_t)k0 * g.K + q0;
-            t.out = g.out + ((int64_t)e * g.N + p0) * g.K + q0;
-        }
-        t.rows = __builtin_amdgcn_readfirstlane(t.rows);
-        t.cols = __builtin_amdgcn_readfirstlane(t.cols);
-        t.nk = __builtin_amdgcn_readfirstlane(t.nk);
-        t.p = (const uint8_t*)uniform_ptr(t.p);
-        t.q = (const uint8_t*)uniform_ptr(t.q);
-        t.ps = (const uint8_t*)uniform_ptr(t.ps);
-        t.qs = (const uint8_t*)uniform_ptr(t.qs);
-        t.out = (uint16_t*)uniform_ptr(t.out);
-        return t;
     }
 };
 
-// The load side: walks the workgroup's K steps STAGES - 1 ahead of the sums.
+// The load side: walks the workgroup's K steps ahead of the sums.  Behind the
+// last step it stays there and loads it again and again (into LDS that nobody
+// reads any more), so that every wave has LOADS loads a step in flight to count.
 template <class C>
 struct Loader {
-    Tile t;
-    int k;
-    int64_t idx, end, step;
-    bool live;
-    uint32_t po[C::PP], qo[C::QP], so;        // byte offsets from the tile's bases
-    int sp_at[C::TT], sq_at[C::J];            // wgrad: this lane's scale rows
-    uint32_t sp[C::TT], sq[C::J];             // wgrad: scales of the step issued last
+    const uint8_t* p;  // operands and scales of the step to issue
+    const uint8_t* q;
+    const uint8_t* ps;
+    const uint8_t* qs;
+    int left;  // steps of the tile from this one on; 0: the workgroup has none
+    int n;     // tiles opened
+    uint32_t po[C::PP], qo[C::QP], so;  // this lane's byte offsets, the same for all steps of a tile
 
-    __device__ __forceinline__ void open(const Worker<C>& w) {
-        live = false;
-        while (idx < end) {
-            t = w.at(idx);
-            idx += step;
-            if (t.nk > 0) {
-                live = true;
-                break;
+    __device__ __forceinline__ Loader(const BlockArgs& g, const Place<C>& w, const TileRec* rec, const int* steps,
+                                      int tiles) {
+        n = 0;
+        left = 0;
+        open(g, w, rec, steps, tiles);
+    }
+    // The next tile with a step; nothing changes if there is none.
+    __device__ __forceinline__ void open(const BlockArgs& g, const Place<C>& w, const TileRec* rec, const int* steps,
+                                         int tiles) {
+        while (n < tiles) {
+            Tile<C> t;
+            t.read(g, rec, steps, n++);
+            if (t.nk == 0) continue;
+            left = t.nk;
+            const int q0 = t.w * C::BQ;
+            if (C::MODE == kProduct) {
+                const int kb = g.K / kBK, nb = (g.N + 127) / 128;
+                p = g.p + (int64_t)t.x * g.ld;
+                q = g.q + ((int64_t)t.z * g.N + q0) * g.ld;
+                ps = (const uint8_t*)((const float*)g.ps + t.x);
+                qs = (const uint8_t*)((const float*)g.qs + ((int64_t)t.z * nb + q0 / 128) * kb);
+            } else {
+                p = g.p + (int64_t)t.x * g.ld + (int64_t)t.y * kBK;
+                q = g.q + (int64_t)q0 * g.ld + (int64_t)t.y * kBK;
+                ps = (const uint8_t*)g.ps + (int64_t)t.y * g.N + t.x;
+                qs = (const uint8_t*)g.qs + (int64_t)t.y * g.K + q0;
             }
+            // Rows past the tile's end read its last row: their sums are never
+            // stored.  Row strides are below 2^24: 24-bit products.
+            const int r = w.tid >> 3;
+            const uint32_t chunk = 16 * ((w.tid & 7) ^ row_key(r)), ld = (uint32_t)g.ld;
+#pragma unroll
+            for (int i = 0; i < C::PP; ++i) po[i] = __umul24((uint32_t)min(r + i * C::ROWS, t.rows - 1), ld) + chunk;
+#pragma unroll
+            for (int i = 0; i < C::QP; ++i)
+                qo[i] = __umul24((uint32_t)min(q_row<C::J>(r + i * C::ROWS), t.cols - 1), ld) + chunk;
+            const bool rw = w.wave < C::BP / 64;
+            if (C::MODE == kProduct) {
+                // waves below BP / 64: 64 row scales each; the others: the scales of the tile's q blocks
+                so = 4u * (uint32_t)(rw ? min(w.wave * 64 + w.lane, t.rows - 1)
+                                        : min(w.lane % ((C::BQ + 127) / 128), (t.cols - 1) / 128) * (g.K / kBK));
+            } else {
+                so = (uint32_t)(rw ? t.rows : t.cols);
+            }
+            return;
         }
-        if (!live) return;
-        k = 0;
-        const int r = w.tid >> 3;
-        const uint32_t ld = (uint32_t)w.g.ld;
-        const int pc = (w.tid & 7) ^ p_key(r), qc = (w.tid & 7) ^ q_key<C::J>(r);
-#pragma unroll
-        for (int i = 0; i < C::PP; ++i) po[i] = (uint32_t)min(r + i * C::ROWS, t.rows - 1) * ld + 16 * pc;
-#pragma unroll
-        for (int i = 0; i < C::QP; ++i) qo[i] = (uint32_t)min(r + i * C::ROWS, t.cols - 1) * ld + 16 * qc;
-        if (C::MODE == kProduct) {
-            // waves below BP / 64: 64 row scales each; the others: the scales of the tile's q blocks
-            const int kb = w.g.K / kBK, qb = min(w.lane % ((C::BQ + 127) / 128), (t.cols - 1) / 128);
-            so = w.wave < C::BP / 64 ? 4u * (uint32_t)min(w.wave * 64 + w.lane, t.rows - 1) : 4u * (uint32_t)(qb * kb);
+    }
+    __device__ __forceinline__ void advance(const BlockArgs& g, const Place<C>& w, const TileRec* rec,
+                                            const int* steps, int tiles) {
+        if (left > 1) {
+            --left;
+            p += kBK;
+            q += kBK;
+            ps += C::MODE == kProduct ? 4 * g.R : (int64_t)g.N;
+            qs += C::MODE == kProduct ? 4 : (int64_t)g.K;
         } else {
-            const int c = w.lane & 31;
-#pragma unroll
-            for (int i = 0; i < C::TT; ++i) sp_at[i] = min((w.wp * C::TT + i) * 32 + c, t.rows - 1);
-#pragma unroll
-            for (int j = 0; j < C::J; ++j)
-                sq_at[j] = min(w.wq * 32 * C::J + (c >> 2) * 4 * C::J + 4 * j + (c & 3), t.cols - 1);
+            open(g, w, rec, steps, tiles);
         }
     }
 
-    // Issue the loads of the next step into `stage` and move on.
-    __device__ __forceinline__ void issue(const Worker<C>& w, int stage) {
-        if (C::MODE == kWgrad) {
-            const uint8_t* a = t.ps + (int64_t)k * w.g.N;
-            const uint8_t* b = t.qs + (int64_t)k * w.g.K;
-#pragma unroll
-            for (int i = 0; i < C::TT; ++i) sp[i] = a[sp_at[i]];
-#pragma unroll
-            for (int j = 0; j < C::J; ++j) sq[j] = b[sq_at[j]];
-        }
-        const uint32_t at = lds_addr(w.lds) + (uint32_t)(stage * C::STAGE) + (uint32_t)w.wave * 1024u;
-        const uint8_t* pb = t.p + (int64_t)k * kBK;
-        const uint8_t* qb = t.q + (int64_t)k * kBK;
-#pragma unroll
-        for (int i = 0; i < C::PP; ++i) dma_x4(at + i * C::THREADS * 16, pb, po[i]);
-#pragma unroll
-        for (int i = 0; i < C::QP; ++i) dma_x4(at + C::QOFF + i * C::THREADS * 16, qb, qo[i]);
+    // Loads of pass i of the step into the stage at `lds`.
+    __device__ __forceinline__ void load_p(const Place<C>& w, uint32_t lds, int i) const {
+        dma_x4(lds + w.wave * 1024 + i * C::THREADS * 16, p, po[i]);
+    }
+    __device__ __forceinline__ void load_q(const Place<C>& w, uint32_t lds, int i) const {
+        dma_x4(lds + C::QOFF + w.wave * 1024 + i * C::THREADS * 16, q, qo[i]);
+    }
+    __device__ __forceinline__ void load_scales(const Place<C>& w, uint32_t lds) const {
+        const bool rw = w.wave < C::BP / 64;
+        const uint8_t* s = rw ? ps : qs;
         if (C::MODE == kProduct) {
-            const uint32_t s = lds_addr(w.lds) + (uint32_t)(stage * C::STAGE + C::SOFF);
-            const bool rows = w.wave < C::BP / 64;
-            const uint8_t* base = rows ? t.ps + 4 * (int64_t)k * w.g.R : t.qs + 4 * (int64_t)k;
-            dma_x1(s + (rows ? (uint32_t)w.wave * 256u : C::BP * 4u), base, so);
+            dma_x1(lds + C::SOFF + (rw ? w.wave * 256 : C::BP * 4), s, so);
+        } else {
+            // 64 bytes of scales each: whole words from the word that holds the
+            // first byte to the word that holds the last (never a word without a byte of it)
+            const int r0 = (rw ? w.wave : w.wave - C::BP / 64) * 64;
+            const int n = __builtin_amdgcn_readfirstlane((int)so) - 1, first = min(r0, n);
+            const int skew = (int)((uintptr_t)(s + first) & 3);
+            const uint32_t last = (uint32_t)(min(r0 + 63, n) - first + skew) / 4;
+            dma_x1(lds + C::SOFF + w.wave * 256, s + first - skew, 4u * min((uint32_t)w.lane, last));
         }
-        if (++k == t.nk) open(w);
+    }
+    __device__ __forceinline__ void load_all(const Place<C>& w, uint32_t lds) const {
+#pragma unroll
+        for (int i = 0; i < C::PP; ++i) load_p(w, lds, i);
+#pragma unroll
+        for (int i = 0; i < C::QP; ++i) load_q(w, lds, i);
+        load_scales(w, lds);
     }
 };
 
+// wgrad: where the scale bytes of a step lie in its stage.  Each wave loaded
+// 64 of them from the word that holds the first, so they start up to 3 bytes in.
 template <class C>
-__global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block(BlockArgs g) {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[C::STAGES * C::STAGE];
-    __shared__ int pre[kMaxGroups + 1];
-    __shared__ int wave_sum[C::WAVES];
-    Worker<C> w(g, lds, pre);
-    const int lane = w.lane;
+struct ScaleSkew {
+    uintptr_t ps, qs;  // addresses of the tile's scales of the current step
+    int rows, cols;
 
-    {  // pre: exclusive prefix sums over the groups
+    __device__ __forceinline__ void open(const BlockArgs& g, const Tile<C>& t) {
+        ps = (uintptr_t)g.ps + (uintptr_t)((int64_t)t.y * g.N + t.x);
+        qs = (uintptr_t)g.qs + (uintptr_t)((int64_t)t.y * g.K + t.w * C::BQ);
+        rows = t.rows;
+        cols = t.cols;
+    }
+    __device__ __forceinline__ void next(const BlockArgs& g) {
+        ps += (uintptr_t)g.N;
+        qs += (uintptr_t)g.K;
+    }
+    // the scale of row r of P or Q (rows past the end: some scale)
+    __device__ __forceinline__ int p(const uint8_t* s, int r) const { return at(s, r, rows, ps); }
+    __device__ __forceinline__ int q(const uint8_t* s, int r) const { return at(s + C::BP / 64 * 256, r, cols, qs); }
+
+private:
+    __device__ __forceinline__ static int at(const uint8_t* s, int r, int n, uintptr_t base) {
+        r = min(r, n - 1);
+        return s[(r / 64) * 256 + (int)((base + (uintptr_t)(r / 64 * 64)) & 3) + r % 64];
+    }
+};
+
+// The sum side of one wave: operand fragments, scales and, for the product,
+// two partial tiles, so that one tile's scaled adds run while the next tile's
+// MFMAs do.
+template <class C>
+struct Frags {
+    static constexpr int QSETS = C::J < 2 ? 1 : 2;
+    v8i p[C::TT][2], q[QSETS][2];  // q: tile j in set j % QSETS
+    v16f part[2];                  // product
+    float sc[C::TT], late;         // product: the step's scales; that of the pending partial tile
+    int sp[C::TT], sq[C::J];       // wgrad
+
+    // Chunks 2 i + h, i = 0..3, of a row lie at its chunk h ^ key with i's bits
+    // flipped on top, so one offset and three XORs reach all four (stages and
+    // rows are multiples of 128 bytes).
+    __device__ __forceinline__ static v8i frag(const uint8_t* lds, uint32_t at, int s, int row) {
+        const v4i x = *reinterpret_cast<const v4i*>(lds + (at ^ (uint32_t)(s << 6)) + row * kBK);
+        const v4i y = *reinterpret_cast<const v4i*>(lds + (at ^ (uint32_t)(s << 6 | 32)) + row * kBK);
+        return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    __device__ __forceinline__ void read_p(const uint8_t* lds, uint32_t at) {
+#pragma unroll
+        for (int i = 0; i < C::TT; ++i)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) p[i][s] = frag(lds, at, s, 32 * i);
+    }
+    __device__ __forceinline__ void read_q(const uint8_t* lds, uint32_t at, int j) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) q[j % QSETS][s] = frag(lds, at, s, 32 * j);
+    }
+    // The scales of the step in the stage at b; prow: this lane's first row of
+    // the tile; k: where the bytes start (wgrad).
+    __device__ __forceinline__ void read_scales(const Place<C>& w, const uint8_t* b, const ScaleSkew<C>& k, int prow) {
+        if (C::MODE == kProduct) {
+            const float* s = reinterpret_cast<const float*>(b + C::SOFF);
+            const float qs = s[C::BP + w.wq * 32 * C::J / 128];
+#pragma unroll
+            for (int i = 0; i < C::TT; ++i) sc[i] = s[prow + 32 * i] * qs;
+        } else {
+            const uint8_t* s = b + C::SOFF;
+#pragma unroll
+            for (int i = 0; i < C::TT; ++i) sp[i] = k.p(s, prow + 32 * i);
+#pragma unroll
+            for (int j = 0; j < C::J; ++j) sq[j] = k.q(s, q_row<C::J>((w.wq * C::J + j) * 32 + (w.lane & 31)));
+        }
+    }
+    __device__ __forceinline__ void clear() {
+        if (C::MODE == kProduct) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) part[1][r] = 0.f;
+            late = 0.f;
+        }
+    }
+    // The empty asm statements keep sums and MFMAs where they are written: the
+    // compiler would sink them behind the next branch, with all their operands
+    // alive until there.
+    __device__ __forceinline__ void multiply(v16f (&acc)[C::J][C::TT], int j, int i) {
+        constexpr int U = C::J * C::TT;
+        static_assert(U % 2 == 0, "partial tiles alternate");
+        if (C::MODE == kProduct) {
+            const int u = j * C::TT + i, v = (u + U - 1) % U;  // the pending unit
+            v16f n = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+            n = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(q[j % QSETS][0], p[i][0], n, 0, 0, 0, 0, 0, 0);
+            asm volatile("" : "+v"(n));
+            __builtin_amdgcn_sched_barrier(0);
+            // half of the pending adds behind each MFMA: a 64-cycle MFMA leaves
+            // a wave about 15 issue slots
+#pragma unroll
+            for (int r = 0; r < 8; ++r) acc[v / C::TT][v % C::TT][r] += part[(u + 1) & 1][r] * late;
+            asm volatile("" : "+v"(acc[v / C::TT][v % C::TT]));
+            __builtin_amdgcn_sched_barrier(0);
+            n = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(q[j % QSETS][1], p[i][1], n, 0, 0, 0, 0, 0, 0);
+            asm volatile("" : "+v"(n));
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = 8; r < 16; ++r) acc[v / C::TT][v % C::TT][r] += part[(u + 1) & 1][r] * late;
+            asm volatile("" : "+v"(acc[v / C::TT][v % C::TT]));
+            __builtin_amdgcn_sched_barrier(0);
+            part[u & 1] = n;
+            late = sc[i];
+        } else {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(q[j % QSETS][s], p[i][s], acc[j][i], 0, 0, 0,
+                                                                            sq[j], 0, sp[i]);
+            asm volatile("" : "+v"(acc[j][i]));
+        }
+    }
+    __device__ __forceinline__ void finish(v16f (&acc)[C::J][C::TT]) {
+        if (C::MODE == kProduct) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[C::J - 1][C::TT - 1][r] += part[1][r] * late;
+        }
+    }
+};
+
+// Fills `table` with the workgroup's tile records; their number, 0 if it has none.
+template <class C>
+__device__ __forceinline__ int plan_tiles(const BlockArgs& g, const Place<C>& w, int* table, int* wave_sum) {
+    int* pre = table;  // exclusive prefix sums over the groups, before the records
+    {
         constexpr int kPer = kMaxGroups / C::THREADS;
         constexpr int kUnit = C::MODE == kProduct ? C::BP : kBK;
         int n[kPer], sum = 0;
@@ -292,9 +458,9 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block(
         int before = sum;
         for (int d = 1; d < kWave; d <<= 1) {
             const int up = __shfl_up(before, d);
-            before += lane >= d ? up : 0;
+            before += w.lane >= d ? up : 0;
         }
-        if (lane == kWave - 1) wave_sum[w.wave] = before;
+        if (w.lane == kWave - 1) wave_sum[w.wave] = before;
         __syncthreads();
         before -= sum;
         for (int v = 0; v < w.wave; ++v) before += wave_sum[v];
@@ -307,161 +473,245 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block(
         if (w.tid == C::THREADS - 1 && g.E == kMaxGroups) pre[kMaxGroups] = before;
         __syncthreads();
     }
-
     // XCD x (workgroups go round-robin over the 8) takes the x-th contiguous
-    // eighth of the tile order, so that its L2 sees neighbouring tiles.
-    const int64_t total = w.tiles();
-    const int xcd = blockIdx.x & 7;
-    const int64_t step = gridDim.x / 8, end = total * (xcd + 1) / 8;
-    int64_t idx = total * xcd / 8 + (blockIdx.x >> 3);
-    if (idx >= end) return;
-
-    Loader<C> ld;
-    ld.idx = idx;
-    ld.end = end;
-    ld.step = step;
-    ld.open(w);
-    int ahead = 0;   // stages issued and not yet used
-    int stage = 0;   // next stage to use
-#pragma unroll
-    for (int s = 0; s < C::STAGES - 1; ++s)
-        if (ld.live) {
-            ld.issue(w, s);
-            ++ahead;
-        }
-
-    // LDS read offsets: the four 16-byte chunks of this lane's half
-    const int c = lane & 31, h = lane >> 5;
-    const int prow = w.wp * 32 * C::TT + c;
-    const int qrow = w.wq * 32 * C::J + (c >> 2) * 4 * C::J + (c & 3);
-    uint32_t pr[4], qr[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        pr[i] = prow * kBK + (((2 * i + h) ^ p_key(prow)) << 4);
-        qr[i] = C::QOFF + qrow * kBK + (((2 * i + h) ^ q_key<C::J>(qrow)) << 4);
+    // eighth of the tile order, so that its L2 sees neighbouring tiles; its
+    // workgroups take them in turn, at most THREADS each (the launch sees to it).
+    const Order<C> o(g, pre);
+    const uint32_t xcd = blockIdx.x & 7, step = gridDim.x / 8;
+    const uint32_t end = (uint32_t)((uint64_t)o.total * (xcd + 1) / 8);
+    const uint32_t idx = (uint32_t)((uint64_t)o.total * xcd / 8) + (blockIdx.x >> 3);
+    if (idx >= end) return 0;
+    const int ntiles = __builtin_amdgcn_readfirstlane((int)((end - idx + step - 1) / step));
+    TileRec t = {0, 0, 0, 0};
+    int nk = 0;
+    if (w.tid < ntiles) {
+        t = o.at(g, pre, idx + (uint32_t)w.tid * step);
+        if (C::MODE == kWgrad) nk = clamp_int(pre[t.z + 1], t.y, (int)(g.ld / kBK)) - t.y;
     }
+    __syncthreads();
+    if (w.tid < ntiles) {
+        reinterpret_cast<TileRec*>(table)[w.tid] = t;
+        if (C::MODE == kWgrad) table[4 * C::THREADS + w.tid] = nk;
+    }
+    __syncthreads();
+    return ntiles;
+}
 
-    for (; idx < end; idx += step) {
-        const Tile t = w.at(idx);
+// Rounds the wave's sums to bf16 and stores them.  Lane: row prow + 32 i of
+// the tile; register 4a + b of tile j is output (2a + h) * 4J + 4j + b of the
+// wave's 32 J.
+template <class C>
+__device__ __forceinline__ void store(const BlockArgs& g, const Place<C>& w, const Tile<C>& t, int prow,
+                                      const v16f (&acc)[C::J][C::TT]) {
+    const int h = w.lane >> 5;
+    const int64_t ldo = C::MODE == kProduct ? g.N : g.K;
+#pragma unroll
+    for (int i = 0; i < C::TT; ++i) {
+        if (prow + 32 * i >= t.rows) continue;
+        uint16_t* o = t.out(g) + (prow + 32 * i) * ldo;
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            const int q = w.wq * 32 * C::J + (2 * a + h) * 4 * C::J;
+            if (C::J % 2 == 0 && g.wide) {
+#pragma unroll
+                for (int j = 0; j + 1 < C::J; j += 2) {
+                    const uint4 v = make_uint4(pack_bf16x2(acc[j][i][4 * a], acc[j][i][4 * a + 1]),
+                                               pack_bf16x2(acc[j][i][4 * a + 2], acc[j][i][4 * a + 3]),
+                                               pack_bf16x2(acc[j + 1][i][4 * a], acc[j + 1][i][4 * a + 1]),
+                                               pack_bf16x2(acc[j + 1][i][4 * a + 2], acc[j + 1][i][4 * a + 3]));
+                    if (q + 4 * j < t.cols) *reinterpret_cast<uint4*>(o + q + 4 * j) = v;
+                }
+            } else if (g.wide) {
+#pragma unroll
+                for (int j = 0; j < C::J; ++j) {
+                    const uint2 v = make_uint2(pack_bf16x2(acc[j][i][4 * a], acc[j][i][4 * a + 1]),
+                                               pack_bf16x2(acc[j][i][4 * a + 2], acc[j][i][4 * a + 3]));
+                    if (q + 4 * j < t.cols) *reinterpret_cast<uint2*>(o + q + 4 * j) = v;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < C::J; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (q + 4 * j + x < t.cols)
+                            o[q + 4 * j + x] = (uint16_t)pack_bf16x2(acc[j][i][4 * a + x], 0.f);
+            }
+        }
+    }
+}
+
+template <class C>
+__device__ __forceinline__ void clear_sums(v16f (&acc)[C::J][C::TT], Frags<C>& f) {
+#pragma unroll
+    for (int j = 0; j < C::J; ++j)
+#pragma unroll
+        for (int i = 0; i < C::TT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.f;
+    f.clear();
+}
+
+// Many rows a group.  Eight waves, two on each SIMD: waves 0-3 and waves 4-7
+// go through the same four phases of a K step - read fragments of half the
+// step from LDS, multiply, read the other half, multiply - one phase apart, so
+// that on every SIMD one wave's MFMAs run while the other reads.  The direct
+// loads go out between the MFMAs.  With both waves in the same phase the MFMAs
+// were busy for 51 % of the time.
+//
+// Barriers.  Phase f (0..3) of step n lies between barriers 4n + f and
+// 4n + f + 1 for the first waves and one later for the others (they meet once
+// more at the start, the first waves once more at the end).
+//   P, the scales and Q tiles 0, 1 of a stage are read in phase 0, by barrier
+//   4n + 2; their loads for step n + 2 go out in phase 3, after barrier
+//   4n + 3, and are waited for in phase 2 of step n + 1, before 4n + 8.
+//   Q tiles 2, 3 are read in phase 2, by barrier 4n + 4; their loads for step
+//   n + 2 go out in phase 1 of step n + 1, after 4n + 5, and are waited for in
+//   phase 0 of step n + 2, before 4n + 10.
+// Each wait leaves the loads issued since in flight: two, or seven.
+template <class C>
+__global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block(BlockArgs g) {
+    static_assert(C::WAVES == 8 && C::STAGES == 2 && C::J == 4 && C::TT == 2 && C::PP == 4 && C::QP == 4, "");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[C::STAGES * C::STAGE];
+    __shared__ __attribute__((aligned(16))) int table[C::TABLE];
+    __shared__ int wave_sum[C::WAVES];
+    const Place<C> w;
+    const int ntiles = plan_tiles(g, w, table, wave_sum);
+    if (ntiles == 0) return;
+    const TileRec* rec = reinterpret_cast<const TileRec*>(table);
+    const int* steps = table + 4 * C::THREADS;
+    const bool first = w.wave < 4;
+
+    const int c = w.lane & 31, h = w.lane >> 5;
+    const int prow = w.wp * 32 * C::TT + c, qrow = w.wq * 32 * C::J + c;
+    const uint32_t pr = prow * kBK + ((h ^ row_key(prow)) << 4);
+    const uint32_t qr = C::QOFF + qrow * kBK + ((h ^ row_key(qrow)) << 4);
+
+    const uint32_t base = lds_addr(lds);
+    Loader<C> ld(g, w, rec, steps, ntiles);
+    if (ld.left) {
+        ld.load_all(w, base);
+        ld.advance(g, w, rec, steps, ntiles);
+        wait_loads<0>();
+#pragma unroll
+        for (int i = 0; i < C::PP; ++i) ld.load_p(w, base + C::STAGE, i);
+        ld.load_q(w, base + C::STAGE, 0);
+        ld.load_q(w, base + C::STAGE, 2);
+        ld.load_scales(w, base + C::STAGE);
+    }
+    meet();
+    if (!first) meet();
+
+    Frags<C> f;
+    uint32_t stage = 0;  // LDS offset of the current step's stage
+    for (int n = 0; n < ntiles; ++n) {
+        Tile<C> t;
+        t.read(g, rec, steps, n);
+        ScaleSkew<C> skew;
+        skew.open(g, t);
         v16f acc[C::J][C::TT];
-#pragma unroll
-        for (int j = 0; j < C::J; ++j)
-#pragma unroll
-            for (int i = 0; i < C::TT; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.f;
-        // waves whose rows are all past the tile's end only load and meet
-        const bool mine = w.wp * 32 * C::TT < t.rows;
+        clear_sums(acc, f);
 
         for (int k = 0; k < t.nk; ++k) {
-            if (C::STAGES > 2 && ahead == C::STAGES - 1) wait_and_meet<C::LOADS*(C::STAGES - 2)>();
-            else wait_and_meet<0>();
-            uint32_t sp[C::TT], sq[C::J];
-            if (C::MODE == kWgrad) {
-                // taken over before the next loads go out, so that the wait for
-                // them is the one above
-#pragma unroll
-                for (int i = 0; i < C::TT; ++i) {
-                    sp[i] = ld.sp[i];
-                    asm volatile("" : "+v"(sp[i]));
-                }
-#pragma unroll
-                for (int j = 0; j < C::J; ++j) {
-                    sq[j] = ld.sq[j];
-                    asm volatile("" : "+v"(sq[j]));
-                }
-            }
-            if (ld.live) {
-                ld.issue(w, stage == 0 ? C::STAGES - 1 : stage - 1);
-                ++ahead;
-            }
-            const uint8_t* b = lds + stage * C::STAGE;
-            if (mine) {
-                v8i pf[C::TT][2];
-#pragma unroll
-                for (int i = 0; i < C::TT; ++i)
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const v4i x = *reinterpret_cast<const v4i*>(b + pr[2 * s] + i * 32 * kBK);
-                        const v4i y = *reinterpret_cast<const v4i*>(b + pr[2 * s + 1] + i * 32 * kBK);
-                        pf[i][s] = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-                    }
-                float sc[C::TT];
-                if (C::MODE == kProduct) {
-                    const float* s = reinterpret_cast<const float*>(b + C::SOFF);
-                    const float q = s[C::BP + w.wq * 32 * C::J / 128];
-#pragma unroll
-                    for (int i = 0; i < C::TT; ++i) sc[i] = s[prow + 32 * i] * q;
-                }
-#pragma unroll
-                for (int j = 0; j < C::J; ++j) {
-                    v8i qf[2];
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const v4i x = *reinterpret_cast<const v4i*>(b + qr[2 * s] + 4 * j * kBK);
-                        const v4i y = *reinterpret_cast<const v4i*>(b + qr[2 * s + 1] + 4 * j * kBK);
-                        qf[s] = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-                    }
-#pragma unroll
-                    for (int i = 0; i < C::TT; ++i) {
-                        if (C::MODE == kProduct) {
-                            v16f part = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-                            part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(qf[0], pf[i][0], part, 0, 0, 0, 0, 0, 0);
-                            part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(qf[1], pf[i][1], part, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) acc[j][i][r] += part[r] * sc[i];
-                        } else {
-#pragma unroll
-                            for (int s = 0; s < 2; ++s)
-                                acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                    qf[s], pf[i][s], acc[j][i], 0, 0, 0, (int)sq[j], 0, (int)sp[i]);
-                        }
-                    }
-                }
-            }
-            stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-            --ahead;
-        }
+            const uint32_t here = base + stage, there = base + (stage ^ (uint32_t)C::STAGE);
+            f.read_p(lds, pr + stage);
+            f.read_q(lds, qr + stage, 0);
+            f.read_q(lds, qr + stage, 1);
+            f.read_scales(w, lds + stage, skew, prow);
+            wait_and_meet<7>();
+            __builtin_amdgcn_s_setprio(1);
+            f.multiply(acc, 0, 0);
+            ld.load_q(w, there, 1);
+            f.multiply(acc, 0, 1);
+            f.multiply(acc, 1, 0);
+            ld.load_q(w, there, 3);
+            f.multiply(acc, 1, 1);
+            __builtin_amdgcn_s_setprio(0);
+            meet();
 
-        // lane: row prow + 32 i of the tile; register 4a + b of tile j is
-        // output (2a + h) * 4J + 4j + b of the wave's 32 J
-        if (mine) {
-            const int64_t ldo = C::MODE == kProduct ? g.N : g.K;
-#pragma unroll
-            for (int i = 0; i < C::TT; ++i) {
-                if (prow + 32 * i >= t.rows) continue;
-                uint16_t* o = t.out + (prow + 32 * i) * ldo;
-#pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    const int q = w.wq * 32 * C::J + (2 * a + h) * 4 * C::J;
-                    if (C::J % 2 == 0 && g.wide) {
-#pragma unroll
-                        for (int j = 0; j + 1 < C::J; j += 2) {
-                            const uint4 v = make_uint4(pack_bf16x2(acc[j][i][4 * a], acc[j][i][4 * a + 1]),
-                                                       pack_bf16x2(acc[j][i][4 * a + 2], acc[j][i][4 * a + 3]),
-                                                       pack_bf16x2(acc[j + 1][i][4 * a], acc[j + 1][i][4 * a + 1]),
-                                                       pack_bf16x2(acc[j + 1][i][4 * a + 2], acc[j + 1][i][4 * a + 3]));
-                            if (q + 4 * j < t.cols) *reinterpret_cast<uint4*>(o + q + 4 * j) = v;
-                        }
-                    } else if (g.wide) {
-#pragma unroll
-                        for (int j = 0; j < C::J; ++j) {
-                            const uint2 v = make_uint2(pack_bf16x2(acc[j][i][4 * a], acc[j][i][4 * a + 1]),
-                                                       pack_bf16x2(acc[j][i][4 * a + 2], acc[j][i][4 * a + 3]));
-                            if (q + 4 * j < t.cols) *reinterpret_cast<uint2*>(o + q + 4 * j) = v;
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < C::J; ++j)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                if (q + 4 * j + x < t.cols)
-                                    o[q + 4 * j + x] = (uint16_t)pack_bf16x2(acc[j][i][4 * a + x], 0.f);
-                    }
-                }
-            }
+            f.read_q(lds, qr + stage, 2);
+            f.read_q(lds, qr + stage, 3);
+            ld.advance(g, w, rec, steps, ntiles);
+            wait_and_meet<2>();
+            __builtin_amdgcn_s_setprio(1);
+            f.multiply(acc, 2, 0);
+            ld.load_p(w, here, 0);
+            ld.load_p(w, here, 1);
+            f.multiply(acc, 2, 1);
+            ld.load_p(w, here, 2);
+            ld.load_p(w, here, 3);
+            f.multiply(acc, 3, 0);
+            ld.load_q(w, here, 0);
+            ld.load_q(w, here, 2);
+            f.multiply(acc, 3, 1);
+            ld.load_scales(w, here);
+            __builtin_amdgcn_s_setprio(0);
+            meet();
+            stage ^= (uint32_t)C::STAGE;
+            skew.next(g);
         }
+        f.finish(acc);
+        store(g, w, t, prow, acc);
     }
+    if (first) meet();
+    wait_loads<0>();  // no load may write LDS once the workgroup is gone
+}
+
+// Few rows a group: the weights' stream bounds it.  64-row tiles, four waves,
+// STAGES K steps in flight, two workgroups on a CU.
+template <class C>
+__global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block_few(BlockArgs g) {
+    static_assert(C::J == 1 && C::MODE == kProduct && C::STAGES == 3, "");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[C::STAGES * C::STAGE];
+    __shared__ __attribute__((aligned(16))) int table[C::TABLE];
+    __shared__ int wave_sum[C::WAVES];
+    const Place<C> w;
+    const int ntiles = plan_tiles(g, w, table, wave_sum);
+    if (ntiles == 0) return;
+    const TileRec* rec = reinterpret_cast<const TileRec*>(table);
+
+    const int c = w.lane & 31, h = w.lane >> 5;
+    const int prow = w.wp * 32 * C::TT + c, qrow = w.wq * 32 + c;
+    const uint32_t pr = prow * kBK + ((h ^ row_key(prow)) << 4);
+    const uint32_t qr = C::QOFF + qrow * kBK + ((h ^ row_key(qrow)) << 4);
+
+    Loader<C> ld(g, w, rec, nullptr, ntiles);
+#pragma unroll
+    for (int s = 0; s < C::STAGES; ++s) {
+        ld.load_all(w, lds_addr(lds) + s * C::STAGE);
+        ld.advance(g, w, rec, nullptr, ntiles);
+    }
+
+    const ScaleSkew<C> skew = {};
+    Frags<C> f;
+    uint32_t stage = 0;  // LDS offset of the current step's stage
+    wait_and_meet<C::LOADS*(C::STAGES - 1)>();
+    f.read_scales(w, lds, skew, prow);
+    f.read_p(lds, pr);
+    f.read_q(lds, qr, 0);
+    for (int n = 0; n < ntiles; ++n) {
+        Tile<C> t;
+        t.read(g, rec, nullptr, n);
+        v16f acc[C::J][C::TT];
+        clear_sums(acc, f);
+        for (int k = 0; k < t.nk; ++k) {
+            const uint32_t next = stage + C::STAGE == C::STAGES * C::STAGE ? 0u : stage + C::STAGE;
+            // the fragments of this stage are in registers: the next stage's
+            // loads are waited for, the workgroup meets, and this stage goes to
+            // the step STAGES ahead
+            wait_and_meet<C::LOADS*(C::STAGES - 2)>();
+            ld.load_all(w, lds_addr(lds) + stage);
+#pragma unroll
+            for (int i = 0; i < C::TT; ++i) f.multiply(acc, 0, i);
+            f.read_p(lds, pr + next);
+            f.read_q(lds, qr + next, 0);
+            f.read_scales(w, lds + next, skew, prow);
+            stage = next;
+            ld.advance(g, w, rec, nullptr, ntiles);
+        }
+        f.finish(acc);
+        store(g, w, t, prow, acc);
+    }
+    wait_loads<0>();  // no load may write LDS once the workgroup is gone
 }
 
 // ---- host -----------------------------------------------------------------------
@@ -473,13 +723,21 @@ template <class C>
 void launch(const BlockArgs& g, int64_t p_tiles, int q, hipStream_t stream) {
     const int64_t most = p_tiles * ((q + C::BQ - 1) / C::BQ);
     const int64_t fill = (int64_t)(device_cus() / 8 * 8) * C::PER_CU;
-    const int64_t grid = most < fill ? (most + 7) / 8 * 8 : fill;
-    hipLaunchKernelGGL(k_block<C>, dim3((unsigned)grid), dim3(C::THREADS), 0, stream, g);
+    int64_t grid = most < fill ? (most + 7) / 8 * 8 : fill;
+    // at most THREADS tiles a workgroup (those beyond the resident ones wait their turn)
+    const int64_t least = ((most + 7) / 8 + C::THREADS - 1) / C::THREADS * 8;
+    if (grid < least) grid = least;
+    if constexpr (C::WAVES == 8)
+        hipLaunchKernelGGL(k_block<C>, dim3((unsigned)grid), dim3(C::THREADS), 0, stream, g);
+    else
+        hipLaunchKernelGGL(k_block_few<C>, dim3((unsigned)grid), dim3(C::THREADS), 0, stream, g);
 }
 
 bool block_shape_ok(const moe_block_shape_t* s) {
     return s->R <= (int64_t(1) << 28) && s->N <= (1 << 20) && s->K <= (1 << 20) && s->E <= kMaxGroups;
 }
+// An upper bound of the tiles of `p` rows in up to 1024 groups: the kernels count them in 32 bits.
+int64_t tiles(int64_t p, int bp, int64_t q) { return (p / bp + kMaxGroups) * ((q + 127) / 128); }
 bool block_shape_valid(const moe_block_shape_t* s, const int32_t* offsets) {
     return s && s->R >= 0 && s->N >= 1 && s->K >= 1 && s->E >= 1 && (offsets || s->E == 1);
 }
@@ -495,6 +753,7 @@ int moe_block_gemm(const moe_block_shape_t* s, const uint8_t* a, const float* a_
                    const float* w_scales, const int32_t* offsets, void* out, moe_stream_t stream) {
     if (!block_shape_valid(s, offsets)) return MOE_ERR_INVALID_ARG;
     if (!block_shape_ok(s) || s->K % kBK) return MOE_ERR_UNSUPPORTED;
+    if (tiles(s->R, 64, s->N) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
     if (s->R == 0) return MOE_OK;
     if (!a || !a_scales || !w || !w_scales || !out) return MOE_ERR_INVALID_ARG;
     if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scales, 4) || !aligned(w_scales, 4) ||
@@ -517,6 +776,7 @@ int moe_block_gemm_wgrad(const moe_block_shape_t* s, const uint8_t* gr, const ui
                          const uint8_t* x_scales, const int32_t* offsets, void* out, moe_stream_t stream) {
     if (!block_shape_valid(s, offsets)) return MOE_ERR_INVALID_ARG;
     if (!block_shape_ok(s) || s->R > (int64_t(1) << 23)) return MOE_ERR_UNSUPPORTED;
+    if (tiles((int64_t)s->E * s->N, 256, s->K) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
     if (!out || (s->R > 0 && (!gr || !g_scales || !x || !x_scales))) return MOE_ERR_INVALID_ARG;
     if (!aligned(gr, 16) || !aligned(x, 16) || !aligned(offsets, 4) || !aligned(out, 2)) return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_DEVICE;

@@ -68,7 +68,7 @@ typedef struct {
     int32_t N; /* output features, 1..2^20 */
     int32_t K; /* input features, a multiple of 128, up to 2^20 */
     int32_t E; /* groups, 1..1024 */
-} moe_block_shape_t;
+} moe_block_shape_t; /* (R/64 + 1024) * N/128 and, for wgrad, (E*N/256 + 1024) * K/128 below 2^31 */
 
 /*
  * out bf16 [R][N]: out[r][n] = sum over k of a[r][k] w[e(r)][n][k], a in rows
