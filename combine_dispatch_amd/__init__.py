@@ -343,38 +343,44 @@ def moe_profile_stop() -> tuple[dict, int]:
 
 
 # ---- router and 8-bit products (include/moe_gate.h, include/moe_block8.h) ----
+# The smallest of these calls take a few microseconds on the GPU, so their
+# checks are one pass of plain comparisons; messages are made on failure only.
 
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise MoeError(MOE_ERR_INVALID_ARG, what)
 
 
-def _dense(what: str, name: str, t, shape: tuple, dtypes: tuple, device) -> None:
-    """A densely packed device tensor of one of the dtypes and the shape (None: any length)."""
-    if (t.dtype not in dtypes or t.device != device or len(t.shape) != len(shape) or not t.is_contiguous()
-            or any(n is not None and n != m for n, m in zip(shape, t.shape))):
-        raise MoeError(MOE_ERR_INVALID_ARG,
-                       f"{what}: {name} must be a dense {' or '.join(str(d) for d in dtypes)} tensor of shape "
-                       f"{shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
-                       f"{'' if t.is_contiguous() else ', strided'}")
+def _dense(what: str, name: str, t, shape: tuple, dtypes: tuple, device: int) -> int:
+    """The address of a densely packed tensor of one of the dtypes and the shape on GPU `device`."""
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    raise MoeError(MOE_ERR_INVALID_ARG,
+                   f"{what}: {name} must be a dense {' or '.join(str(d) for d in dtypes)} tensor of shape {shape} "
+                   f"on GPU {device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                   f"{'' if t.is_contiguous() else ', strided'}")
 
 
-def _on_device(what: str, t):
-    device = t.device
-    if device.type != "cuda":
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: tensors must be on the GPU, got {device}")
+def _gpu_of(what: str, t) -> int:
+    device = t.get_device()
+    if device < 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: tensors must be on the GPU, got {t.device}")
     return device
 
 
-def _call(what: str, device, stream, *args) -> None:
-    """The C entry with the tensors' device current, on `stream` or that device's current one."""
+def _call(what: str, fn, device: int, stream, *args) -> None:
+    """The C entry with GPU `device` current, on `stream` or that GPU's current one."""
     import torch
-    fn = getattr(lib(), what)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(stream))
-    else:
+    if device != torch.cuda.current_device():
         with torch.cuda.device(device):
-            rc = fn(*args, _stream(stream))
+            return _call(what, fn, device, stream, *args)
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif hasattr(torch._C, "_cuda_getCurrentRawStream"):  # without building a Stream object
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        handle = torch.cuda.current_stream().cuda_stream
+    rc = fn(*args, handle)
     if rc != MOE_OK:
         raise MoeError(rc, what)
 
@@ -398,43 +404,50 @@ def _input_dtype(what: str, name: str, t) -> int:
     import torch
     if t.dtype == torch.float32:
         return MOE_DTYPE_F32
-    _need(t.dtype == torch.bfloat16, f"{what}: {name} must be float32 or bfloat16, got {t.dtype}")
-    return MOE_DTYPE_BF16
+    if t.dtype == torch.bfloat16:
+        return MOE_DTYPE_BF16
+    raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: {name} must be float32 or bfloat16, got {t.dtype}")
 
 
 def _gate_call(what, logits, opts, token_mask, K):
+    """(GPU, shape, options, address of the logits, of the mask) of a router call."""
     import torch
-    device = _on_device(what, logits)
+    device = _gpu_of(what, logits)
     _need(logits.dim() == 2, f"{what}: logits must be [T][E]")
     T, E = logits.shape
-    _dense(what, "logits", logits, (T, E), (logits.dtype,), device)
-    o = opts if opts is not None else MoeGateOptions(MOE_DTYPE_F32, MOE_SCORE_SOFTMAX, 1, 1.0)
-    o = MoeGateOptions(_input_dtype(what, "logits", logits), o.score, o.renormalise, o.scale)
+    dtype = _input_dtype(what, "logits", logits)
+    if opts is None:
+        o = MoeGateOptions(dtype, MOE_SCORE_SOFTMAX, 1, 1.0)
+    else:
+        o = MoeGateOptions(dtype, opts.score, opts.renormalise, opts.scale)
+    mask = None
     if token_mask is not None:
-        _dense(what, "token_mask", token_mask, (T,), (torch.uint8, torch.bool), device)
-    return device, MoeGateShape(T, E, K), o
+        mask = _dense(what, "token_mask", token_mask, (T,), (torch.uint8, torch.bool), device)
+    return (device, MoeGateShape(T, E, K), o, _dense(what, "logits", logits, (T, E), (logits.dtype,), device), mask)
 
 
-def _sequences(what, seq_offsets, device) -> int:
+def _offsets(what, name, offsets, device):
+    """(number of ranges, address) of an int32 array of range bounds; (1, None) for None."""
     import torch
-    if seq_offsets is None:
-        return 1
-    _dense(what, "seq_offsets", seq_offsets, (None,), (torch.int32,), device)
-    return seq_offsets.shape[0] - 1
+    if offsets is None:
+        return 1, None
+    n = offsets.shape[0] if offsets.dim() == 1 else 0
+    _need(n >= 2, f"{what}: {name} must hold the bounds of at least one range")
+    return n - 1, _dense(what, name, offsets, (n,), (torch.int32,), device)
 
 
 def moe_gate(logits, topk_idx, topk_w, bias=None, token_mask=None, opts=None, stream=None) -> None:
     """topk_idx (int64), topk_w (fp32) [T][K] <- the top-k gate of logits [T][E]."""
     import torch
+    what = "moe_gate"
     _need(topk_idx.dim() == 2, "moe_gate: topk_idx must be [T][K]")
     K = topk_idx.shape[1]
-    device, shape, o = _gate_call("moe_gate", logits, opts, token_mask, K)
-    _dense("moe_gate", "topk_idx", topk_idx, (shape.T, K), (torch.int64,), device)
-    _dense("moe_gate", "topk_w", topk_w, (shape.T, K), (torch.float32,), device)
-    if bias is not None:
-        _dense("moe_gate", "bias", bias, (shape.E,), (torch.float32,), device)
-    _call("moe_gate", device, stream, shape, o, _ptr(logits), _ptr(bias), _ptr(token_mask), _ptr(topk_idx),
-          _ptr(topk_w))
+    device, shape, o, l, mask = _gate_call(what, logits, opts, token_mask, K)
+    out = (logits.shape[0], K)
+    _call(what, lib().moe_gate, device, stream, shape, o, l,
+          None if bias is None else _dense(what, "bias", bias, (logits.shape[1],), (torch.float32,), device), mask,
+          _dense(what, "topk_idx", topk_idx, out, (torch.int64,), device),
+          _dense(what, "topk_w", topk_w, out, (torch.float32,), device))
 
 
 def moe_gate_backward(logits, dlogits, topk_idx=None, d_topk_w=None, slope=None, d_loss=None, seq_offsets=None,
@@ -446,19 +459,18 @@ def moe_gate_backward(logits, dlogits, topk_idx=None, d_topk_w=None, slope=None,
     _need((topk_idx is None) == (d_topk_w is None), f"{what}: topk_idx and d_topk_w go together")
     _need((slope is None) == (d_loss is None), f"{what}: slope and d_loss go together")
     K = topk_idx.shape[-1] if topk_idx is not None else 1
-    device, shape, o = _gate_call(what, logits, opts, token_mask, K)
-    _dense(what, "dlogits", dlogits, (shape.T, shape.E), (logits.dtype,), device)
+    device, shape, o, l, mask = _gate_call(what, logits, opts, token_mask, K)
+    T, E = logits.shape
+    idx = dw = balance = None
     if topk_idx is not None:
-        _dense(what, "topk_idx", topk_idx, (shape.T, K), (torch.int64,), device)
-        _dense(what, "d_topk_w", d_topk_w, (shape.T, K), (torch.float32,), device)
-    balance = None
+        idx = _dense(what, "topk_idx", topk_idx, (T, K), (torch.int64,), device)
+        dw = _dense(what, "d_topk_w", d_topk_w, (T, K), (torch.float32,), device)
     if slope is not None:
-        S = _sequences(what, seq_offsets, device)
-        _dense(what, "slope", slope, (S, shape.E), (torch.float32,), device)
-        _dense(what, "d_loss", d_loss, (1,), (torch.float32,), device)
-        balance = MoeBalanceGrad(_ptr(slope), _ptr(d_loss), _ptr(seq_offsets), S)
-    _call(what, device, stream, shape, o, _ptr(logits), _ptr(token_mask), _ptr(topk_idx), _ptr(d_topk_w), balance,
-          _ptr(dlogits))
+        S, off = _offsets(what, "seq_offsets", seq_offsets, device)
+        balance = MoeBalanceGrad(_dense(what, "slope", slope, (S, E), (torch.float32,), device),
+                                 _dense(what, "d_loss", d_loss, (1,), (torch.float32,), device), off, S)
+    _call(what, lib().moe_gate_backward, device, stream, shape, o, l, mask, idx, dw, balance,
+          _dense(what, "dlogits", dlogits, (T, E), (logits.dtype,), device))
 
 
 def moe_balance_workspace_bytes(T: int, E: int, K: int, S: int = 1) -> int:
@@ -473,15 +485,15 @@ def moe_balance_loss(logits, topk_idx, coef: float, loss, counts, slope, workspa
     what = "moe_balance_loss"
     _need(topk_idx.dim() == 2, f"{what}: topk_idx must be [T][K]")
     K = topk_idx.shape[1]
-    device, shape, o = _gate_call(what, logits, opts, token_mask, K)
-    S = _sequences(what, seq_offsets, device)
-    _dense(what, "topk_idx", topk_idx, (shape.T, K), (torch.int64,), device)
-    _dense(what, "loss", loss, (1,), (torch.float32,), device)
-    _dense(what, "counts", counts, (S, shape.E), (torch.int32,), device)
-    _dense(what, "slope", slope, (S, shape.E), (torch.float32,), device)
-    _dense(what, "workspace", workspace, (None,), (torch.uint8,), device)
-    _call(what, device, stream, shape, o, _ptr(logits), _ptr(token_mask), _ptr(topk_idx), _ptr(seq_offsets), S,
-          float(coef), _ptr(loss), _ptr(counts), _ptr(slope), _ptr(workspace), workspace.shape[0])
+    device, shape, o, l, mask = _gate_call(what, logits, opts, token_mask, K)
+    T, E = logits.shape
+    S, off = _offsets(what, "seq_offsets", seq_offsets, device)
+    _call(what, lib().moe_balance_loss, device, stream, shape, o, l, mask,
+          _dense(what, "topk_idx", topk_idx, (T, K), (torch.int64,), device), off, S, coef,
+          _dense(what, "loss", loss, (1,), (torch.float32,), device),
+          _dense(what, "counts", counts, (S, E), (torch.int32,), device),
+          _dense(what, "slope", slope, (S, E), (torch.float32,), device),
+          _dense(what, "workspace", workspace, (workspace.numel(),), (torch.uint8,), device), workspace.numel())
 
 
 def moe_padded_rows(R: int, E: int = 1) -> int:
@@ -502,15 +514,15 @@ def moe_quantise_rows(x, codes, scales, rows_used=None, stream=None) -> None:
     """codes [R][C'], scales fp32 [C'/128][R] <- x [R][C] (float32 or bfloat16)."""
     import torch
     what = "moe_quantise_rows"
-    device = _on_device(what, x)
+    device = _gpu_of(what, x)
     _need(x.dim() == 2, f"{what}: x must be [R][C]")
     R, C = x.shape
-    _dense(what, "x", x, (R, C), (x.dtype,), device)
-    _dense(what, "codes", codes, (R, _up128(C)), _code_types(), device)
-    _dense(what, "scales", scales, (_up128(C) // 128, R), (torch.float32,), device)
-    if rows_used is not None:
-        _dense(what, "rows_used", rows_used, (1,), (torch.int32,), device)
-    _call(what, device, stream, R, C, _input_dtype(what, "x", x), _ptr(x), _ptr(rows_used), _ptr(codes), _ptr(scales))
+    Cp = _up128(C)
+    _call(what, lib().moe_quantise_rows, device, stream, R, C, _input_dtype(what, "x", x),
+          _dense(what, "x", x, (R, C), (x.dtype,), device),
+          None if rows_used is None else _dense(what, "rows_used", rows_used, (1,), (torch.int32,), device),
+          _dense(what, "codes", codes, (R, Cp), _code_types(), device),
+          _dense(what, "scales", scales, (Cp // 128, R), (torch.float32,), device))
 
 
 def moe_quantise_weights(w, codes, scales, codes_t=None, scales_t=None, stream=None) -> None:
@@ -518,59 +530,52 @@ def moe_quantise_weights(w, codes, scales, codes_t=None, scales_t=None, stream=N
     codes_t [E][K][N'], scales_t [E][K'/128][N'/128] those of the transpose too."""
     import torch
     what = "moe_quantise_weights"
-    device = _on_device(what, w)
+    device = _gpu_of(what, w)
     _need(w.dim() == 3, f"{what}: w must be [E][N][K]")
     E, N, K = w.shape
     Np, Kp = _up128(N), _up128(K)
-    _dense(what, "w", w, (E, N, K), (w.dtype,), device)
-    _dense(what, "codes", codes, (E, N, Kp), _code_types(), device)
-    _dense(what, "scales", scales, (E, Np // 128, Kp // 128), (torch.float32,), device)
     _need((codes_t is None) == (scales_t is None), f"{what}: codes_t and scales_t go together")
+    ct = st = None
     if codes_t is not None:
-        _dense(what, "codes_t", codes_t, (E, K, Np), _code_types(), device)
-        _dense(what, "scales_t", scales_t, (E, Kp // 128, Np // 128), (torch.float32,), device)
-    _call(what, device, stream, E, N, K, _input_dtype(what, "w", w), _ptr(w), _ptr(codes), _ptr(scales),
-          _ptr(codes_t), _ptr(scales_t))
-
-
-def _groups(what, offsets, device) -> int:
-    import torch
-    if offsets is None:
-        return 1
-    _dense(what, "offsets", offsets, (None,), (torch.int32,), device)
-    return offsets.shape[0] - 1
+        ct = _dense(what, "codes_t", codes_t, (E, K, Np), _code_types(), device)
+        st = _dense(what, "scales_t", scales_t, (E, Kp // 128, Np // 128), (torch.float32,), device)
+    _call(what, lib().moe_quantise_weights, device, stream, E, N, K, _input_dtype(what, "w", w),
+          _dense(what, "w", w, (E, N, K), (w.dtype,), device),
+          _dense(what, "codes", codes, (E, N, Kp), _code_types(), device),
+          _dense(what, "scales", scales, (E, Np // 128, Kp // 128), (torch.float32,), device), ct, st)
 
 
 def moe_quantise_columns(x, codes, scales, offsets=None, stream=None) -> None:
     """codes [C][R'], UE8M0 scales [R'/128][C] <- x [R][C], R' = moe_padded_rows(R, E)."""
     import torch
     what = "moe_quantise_columns"
-    device = _on_device(what, x)
+    device = _gpu_of(what, x)
     _need(x.dim() == 2, f"{what}: x must be [R][C]")
     R, C = x.shape
-    E = _groups(what, offsets, device)
+    E, off = _offsets(what, "offsets", offsets, device)
     Rp = moe_padded_rows(R, E)
-    _dense(what, "x", x, (R, C), (x.dtype,), device)
-    _dense(what, "codes", codes, (C, Rp), _code_types(), device)
-    _dense(what, "scales", scales, (Rp // 128, C), (torch.uint8,), device)
-    _call(what, device, stream, R, C, E, _input_dtype(what, "x", x), _ptr(x), _ptr(offsets), _ptr(codes), _ptr(scales))
+    _call(what, lib().moe_quantise_columns, device, stream, R, C, E, _input_dtype(what, "x", x),
+          _dense(what, "x", x, (R, C), (x.dtype,), device), off,
+          _dense(what, "codes", codes, (C, Rp), _code_types(), device),
+          _dense(what, "scales", scales, (Rp // 128, C), (torch.uint8,), device))
 
 
 def moe_block_gemm(a, a_scales, w, w_scales, out, offsets=None, stream=None) -> None:
     """out [R][N] (bf16) <- the grouped product of the quantised rows a [R][K] and weights w [E][N][K]."""
     import torch
     what = "moe_block_gemm"
-    device = _on_device(what, a)
+    device = _gpu_of(what, a)
     _need(a.dim() == 2 and w.dim() == 3, f"{what}: a must be [R][K] and w [E][N][K]")
     (R, K), (E, N) = a.shape, w.shape[:2]
-    _need(_groups(what, offsets, device) == E, f"{what}: offsets must hold E + 1 = {E + 1} entries (none: E = 1)")
-    _dense(what, "a", a, (R, K), _code_types(), device)
-    _dense(what, "a_scales", a_scales, (_up128(K) // 128, R), (torch.float32,), device)
-    _dense(what, "w", w, (E, N, K), _code_types(), device)
-    _dense(what, "w_scales", w_scales, (E, _up128(N) // 128, _up128(K) // 128), (torch.float32,), device)
-    _dense(what, "out", out, (R, N), (torch.bfloat16, torch.int16), device)
-    _call(what, device, stream, MoeBlockShape(R, N, K, E), _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales),
-          _ptr(offsets), _ptr(out))
+    groups, off = _offsets(what, "offsets", offsets, device)
+    if groups != E:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: offsets must hold E + 1 = {E + 1} entries (none: E = 1)")
+    _call(what, lib().moe_block_gemm, device, stream, MoeBlockShape(R, N, K, E),
+          _dense(what, "a", a, (R, K), _code_types(), device),
+          _dense(what, "a_scales", a_scales, (_up128(K) // 128, R), (torch.float32,), device),
+          _dense(what, "w", w, (E, N, K), _code_types(), device),
+          _dense(what, "w_scales", w_scales, (E, _up128(N) // 128, _up128(K) // 128), (torch.float32,), device), off,
+          _dense(what, "out", out, (R, N), (torch.bfloat16, torch.int16), device))
 
 
 def moe_block_gemm_wgrad(g, g_scales, x, x_scales, out, rows: int, offsets=None, stream=None) -> None:
@@ -578,15 +583,14 @@ def moe_block_gemm_wgrad(g, g_scales, x, x_scales, out, rows: int, offsets=None,
     rows: R, the rows the columns layouts were made from."""
     import torch
     what = "moe_block_gemm_wgrad"
-    device = _on_device(what, g)
-    E = _groups(what, offsets, device)
-    Rp = moe_padded_rows(rows, E)
+    device = _gpu_of(what, g)
     _need(g.dim() == 2 and x.dim() == 2, f"{what}: g must be [N][R'] and x [K][R']")
+    E, off = _offsets(what, "offsets", offsets, device)
+    Rp = moe_padded_rows(rows, E)
     N, K = g.shape[0], x.shape[0]
-    _dense(what, "g", g, (N, Rp), _code_types(), device)
-    _dense(what, "g_scales", g_scales, (Rp // 128, N), (torch.uint8,), device)
-    _dense(what, "x", x, (K, Rp), _code_types(), device)
-    _dense(what, "x_scales", x_scales, (Rp // 128, K), (torch.uint8,), device)
-    _dense(what, "out", out, (E, N, K), (torch.bfloat16, torch.int16), device)
-    _call(what, device, stream, MoeBlockShape(rows, N, K, E), _ptr(g), _ptr(g_scales), _ptr(x), _ptr(x_scales),
-          _ptr(offsets), _ptr(out))
+    _call(what, lib().moe_block_gemm_wgrad, device, stream, MoeBlockShape(rows, N, K, E),
+          _dense(what, "g", g, (N, Rp), _code_types(), device),
+          _dense(what, "g_scales", g_scales, (Rp // 128, N), (torch.uint8,), device),
+          _dense(what, "x", x, (K, Rp), _code_types(), device),
+          _dense(what, "x_scales", x_scales, (Rp // 128, K), (torch.uint8,), device), off,
+          _dense(what, "out", out, (E, N, K), (torch.bfloat16, torch.int16), device))

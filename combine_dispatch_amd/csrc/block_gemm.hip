@@ -254,8 +254,10 @@ struct Loader {
             }
             // Rows past the tile's end read its last row: their sums are never
             // stored.  Row strides are below 2^24: 24-bit products.
-            const int r = w.tid >> 3;
-            const uint32_t chunk = 16 * ((w.tid & 7) ^ row_key(r)), ld = (uint32_t)g.ld;
+            int tid = w.tid;
+            asm volatile("" : "+v"(tid));  // as in store()
+            const int r = tid >> 3, lane = tid & 63;
+            const uint32_t chunk = 16 * ((tid & 7) ^ row_key(r)), ld = (uint32_t)g.ld;
 #pragma unroll
             for (int i = 0; i < C::PP; ++i) po[i] = __umul24((uint32_t)min(r + i * C::ROWS, t.rows - 1), ld) + chunk;
 #pragma unroll
@@ -264,8 +266,8 @@ struct Loader {
             const bool rw = w.wave < C::BP / 64;
             if (C::MODE == kProduct) {
                 // waves below BP / 64: 64 row scales each; the others: the scales of the tile's q blocks
-                so = 4u * (uint32_t)(rw ? min(w.wave * 64 + w.lane, t.rows - 1)
-                                        : min(w.lane % ((C::BQ + 127) / 128), (t.cols - 1) / 128) * (g.K / kBK));
+                so = 4u * (uint32_t)(rw ? min(w.wave * 64 + lane, t.rows - 1)
+                                        : min(lane % ((C::BQ + 127) / 128), (t.cols - 1) / 128) * (g.K / kBK));
             } else {
                 so = (uint32_t)(rw ? t.rows : t.cols);
             }
@@ -501,9 +503,11 @@ __device__ __forceinline__ int plan_tiles(const BlockArgs& g, const Place<C>& w,
 // the tile; register 4a + b of tile j is output (2a + h) * 4J + 4j + b of the
 // wave's 32 J.
 template <class C>
-__device__ __forceinline__ void store(const BlockArgs& g, const Place<C>& w, const Tile<C>& t, int prow,
+__device__ __forceinline__ void store(const BlockArgs& g, const Place<C>& w, const Tile<C>& t,
                                       const v16f (&acc)[C::J][C::TT]) {
-    const int h = w.lane >> 5;
+    int lane = w.lane;
+    asm volatile("" : "+v"(lane));  // nothing below is worked out ahead of the K loop and kept through it
+    const int h = lane >> 5, prow = w.wp * 32 * C::TT + (lane & 31);
     const int64_t ldo = C::MODE == kProduct ? g.N : g.K;
 #pragma unroll
     for (int i = 0; i < C::TT; ++i) {
@@ -650,7 +654,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block(
             skew.next(g);
         }
         f.finish(acc);
-        store(g, w, t, prow, acc);
+        store(g, w, t, acc);
     }
     if (first) meet();
     wait_loads<0>();  // no load may write LDS once the workgroup is gone
@@ -709,7 +713,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block_
             ld.advance(g, w, rec, nullptr, ntiles);
         }
         f.finish(acc);
-        store(g, w, t, prow, acc);
+        store(g, w, t, acc);
     }
     wait_loads<0>();  // no load may write LDS once the workgroup is gone
 }
