@@ -718,6 +718,142 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block_
     wait_loads<0>();  // no load may write LDS once the workgroup is gone
 }
 
+// A handful of rows and too few tiles to fill the GPU: one workgroup per 16
+// outputs.  Its eight waves share K (wave v takes blocks v, v + 8, ...), each
+// reading its weights and rows straight into registers, U blocks ahead of those
+// it multiplies (few enough registers for two workgroups on a CU: U = 2 beat 4
+// by up to 2x where there are more workgroups than CUs), and the eight partial sums meet in LDS in a fixed order.
+// One v_mfma_f32_16x16x128_f8f6f4 is one block of 128, so the scales apply to
+// its four results.  Bound by the weights' stream and its latency.
+constexpr int kThinWaves = 8;
+
+template <int MT, int U>
+struct ThinBatch {
+    v4i w[U][2], a[U][MT][2];
+    float sw[U], sa[U][MT];
+};
+
+template <int MT, int U>
+__global__ __launch_bounds__(64 * kThinWaves) void k_block_thin(BlockArgs g) {
+    __shared__ float sums[kThinWaves][MT * 16][17];
+    __shared__ int wave_sum[kThinWaves];
+    __shared__ int found[3];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int e = 0, row0 = 0, rows = 0;
+    if (!g.offsets) {
+        row0 = blockIdx.y * MT * 16;
+        rows = (int)g.R - row0;
+    } else {
+        constexpr int kPer = kMaxGroups / (64 * kThinWaves);
+        int first[kPer], n[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            first[i] = n[i] = 0;
+            if (tid * kPer + i < g.E) group_rows(g, tid * kPer + i, first[i], n[i]);
+            sum += (n[i] + MT * 16 - 1) / (MT * 16);
+        }
+        int before = sum;
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int up = __shfl_up(before, d);
+            before += lane >= d ? up : 0;
+        }
+        if (lane == kWave - 1) wave_sum[wave] = before;
+        if (tid == 0) found[2] = 0;
+        __syncthreads();
+        before -= sum;
+        for (int v = 0; v < wave; ++v) before += wave_sum[v];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int m = (n[i] + MT * 16 - 1) / (MT * 16), at = (int)blockIdx.y - before;
+            if (at >= 0 && at < m) {
+                found[0] = tid * kPer + i;
+                found[1] = first[i] + at * MT * 16;
+                found[2] = n[i] - at * MT * 16;
+            }
+            before += m;
+        }
+        __syncthreads();
+        e = __builtin_amdgcn_readfirstlane(found[0]);
+        row0 = __builtin_amdgcn_readfirstlane(found[1]);
+        rows = __builtin_amdgcn_readfirstlane(found[2]);
+    }
+    if (rows <= 0) return;  // behind the last group's tiles
+    rows = rows < MT * 16 ? rows : MT * 16;
+
+    const int nk = g.K / kBK, n0 = blockIdx.x * 16, c = lane & 15, chunk = lane >> 4;
+    const int nrow = min(n0 + c, g.N - 1);
+    const uint8_t* wp = g.q + ((int64_t)e * g.N + nrow) * g.ld + 16 * chunk;
+    const float* ws = (const float*)g.qs + ((int64_t)e * ((g.N + 127) / 128) + n0 / 128) * nk;
+    const uint8_t* ap[MT];
+    const float* as[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t r = row0 + min(16 * i + c, rows - 1);
+        ap[i] = g.p + r * g.ld + 16 * chunk;
+        as[i] = (const float*)g.ps + r;
+    }
+    // blocks past the last read it again, with a scale of 0
+    auto load = [&](ThinBatch<MT, U>& b, int k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + u * kThinWaves, kc = min(k, nk - 1);
+            const int64_t at = (int64_t)kc * kBK;
+            b.w[u][0] = __builtin_nontemporal_load((const v4i*)(wp + at));
+            b.w[u][1] = __builtin_nontemporal_load((const v4i*)(wp + at + 64));
+            b.sw[u] = k < nk ? ws[kc] : 0.f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                b.a[u][i][0] = *(const v4i*)(ap[i] + at);
+                b.a[u][i][1] = *(const v4i*)(ap[i] + at + 64);
+                b.sa[u][i] = as[i][(int64_t)kc * g.R];
+            }
+        }
+    };
+    v4f acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const ThinBatch<MT, U>& b) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    __builtin_shufflevector(b.w[u][0], b.w[u][1], 0, 1, 2, 3, 4, 5, 6, 7),
+                    __builtin_shufflevector(b.a[u][i][0], b.a[u][i][1], 0, 1, 2, 3, 4, 5, 6, 7), v4f{0.f, 0.f, 0.f, 0.f},
+                    0, 0, 0, 0, 0, 0);
+                const float s = b.sw[u] * b.sa[u][i];
+                // a block past the last adds nothing, whatever it holds
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][r] = b.sw[u] == 0.f ? acc[i][r] : acc[i][r] + part[r] * s;
+            }
+    };
+    ThinBatch<MT, U> x, y;
+    load(x, wave);
+    int k = wave;
+    while (true) {
+        k += U * kThinWaves;
+        if (k < nk) load(y, k);
+        multiply(x);
+        if (k >= nk) break;
+        k += U * kThinWaves;
+        if (k < nk) load(x, k);
+        multiply(y);
+        if (k >= nk) break;
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sums[wave][16 * i + c][4 * chunk + r] = acc[i][r];
+    __syncthreads();
+    for (int i = tid; i < rows * 16; i += 64 * kThinWaves) {
+        const int r = i / 16, n = i % 16;
+        float s = 0.f;
+#pragma unroll
+        for (int v = 0; v < kThinWaves; ++v) s += sums[v][r][n];
+        if (n0 + n < g.N) g.out[(int64_t)(row0 + r) * g.N + n0 + n] = (uint16_t)pack_bf16x2(s, 0.f);
+    }
+}
+
 // ---- host -----------------------------------------------------------------------
 typedef Cfg<kProduct, 2, 4, 4, 2, 2, 4, 1> BigProduct;  // 256 x 256, 8 waves of 64 x 128
 typedef Cfg<kProduct, 4, 1, 1, 2, 3, 1, 2> SmallProduct;  // 64 rows x 128, 4 waves of 64 x 32
@@ -740,6 +876,47 @@ void launch(const BlockArgs& g, int64_t p_tiles, int q, hipStream_t stream) {
 bool block_shape_ok(const moe_block_shape_t* s) {
     return s->R <= (int64_t(1) << 28) && s->N <= (1 << 20) && s->K <= (1 << 20) && s->E <= kMaxGroups;
 }
+template <int MT, int U>
+void launch_thin(const BlockArgs& g, hipStream_t stream) {
+    const int64_t used = g.E < g.R ? g.E : g.R;
+    const int64_t m = g.offsets ? g.R / (16 * MT) + used : (g.R + 16 * MT - 1) / (16 * MT);
+    hipLaunchKernelGGL((k_block_thin<MT, U>), dim3((unsigned)((g.N + 15) / 16), (unsigned)m), dim3(64 * kThinWaves), 0,
+                       stream, g);
+}
+
+// Which kernel a product runs.  Tiles are counted for evenly filled groups
+// (half a tile a group is lost on the last one).  Measured times of a K step:
+// 256 x 256 tiles 1.3 us for up to 256 of them (one per CU), 64 x 128 tiles
+// 0.54 us for up to 256 and then in proportion (1.1 us for 512, two per CU).
+//   one group, K 7168, N 4096: 1024 rows 66 us with small tiles, 76 with large;
+//   2048 rows 129 and 86.  K 2048, N 2048: 2048 rows 20 and 30, 4096 rows 34
+//   and 33.  32 groups, K 7168, N 4096: 64 rows each 175 and 226, 128 rows each
+//   324 and 228.
+// With at most 64 rows a group and few tiles, K is split instead: a round of
+// one 16-output workgroup per CU takes 0.20, 0.30 or 0.45 us for each K step
+// with 16, 32 or 64 rows.
+void launch_product(const BlockArgs& g, hipStream_t stream) {
+    const int64_t used = g.E < g.R ? g.E : g.R, per = (g.R + used - 1) / used, cus = device_cus();
+    const int64_t small = ((g.R + used * 32) / 64 > used ? (g.R + used * 32) / 64 : used) * ((g.N + 127) / 128);
+    const int64_t large = ((g.R + used * 128) / 256 > used ? (g.R + used * 128) / 256 : used) * ((g.N + 255) / 256);
+    const double t_small = 0.54 * (double)(small > cus ? small : cus) / (double)cus;
+    const double t_large = 1.3 * (double)((large + cus - 1) / cus);
+    if (per <= 64) {
+        const int64_t thin = (g.offsets ? g.R / 64 + used : 1) * ((g.N + 15) / 16);
+        const double step = per <= 16 ? 0.15 : per <= 32 ? 0.25 : 0.35;
+        if (step * (double)((thin + cus - 1) / cus) < t_small) {
+            if (per <= 16) launch_thin<1, 2>(g, stream);
+            else if (per <= 32) launch_thin<2, 2>(g, stream);
+            else launch_thin<4, 1>(g, stream);
+            return;
+        }
+    }
+    if (t_small < t_large)
+        launch<SmallProduct>(g, g.R / SmallProduct::BP + used, g.N, stream);
+    else
+        launch<BigProduct>(g, g.R / BigProduct::BP + used, g.N, stream);
+}
+
 // An upper bound of the tiles of `p` rows in up to 1024 groups: the kernels count them in 32 bits.
 int64_t tiles(int64_t p, int bp, int64_t q) { return (p / bp + kMaxGroups) * ((q + 127) / 128); }
 bool block_shape_valid(const moe_block_shape_t* s, const int32_t* offsets) {
@@ -766,13 +943,7 @@ int moe_block_gemm(const moe_block_shape_t* s, const uint8_t* a, const float* a_
     if (!device_ok()) return MOE_ERR_DEVICE;
     BlockArgs g = {a, w, a_scales, w_scales, offsets, static_cast<uint16_t*>(out), s->R, s->K, s->N, s->K, s->E,
                    s->N % 8 == 0 && aligned(out, 16)};
-    const int64_t used = s->E < s->R ? s->E : s->R;
-    // At most 64 rows a group on average: the weights' stream bounds it, and
-    // 64-row tiles waste the least of the matrix cores.
-    if (s->R <= 64 * (int64_t)s->E)
-        launch<SmallProduct>(g, s->R / SmallProduct::BP + used, s->N, stream);
-    else
-        launch<BigProduct>(g, s->R / BigProduct::BP + used, s->N, stream);
+    launch_product(g, stream);
     return launch_status();
 }
 
