@@ -31,39 +31,54 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
     return umax2(v, ror<1>(v));
 }
 
-// 8 values from p[0..n): float32 bit patterns, 0 past n.  VEC: p is 16-byte
-// aligned and n is 8 or nothing.
-template <int DT, bool VEC>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int n, uint32_t (&v)[8]) {
-    if (n <= 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0;
-        return;
+// 16 bytes from p.  VEC: p is 16-byte aligned; else only as its type is, and
+// the hardware splits the access where it has to.  NT: the non-temporal hint.
+template <bool VEC, bool NT>
+__device__ __forceinline__ uint4 load16(const void* p) {
+    if (VEC) {
+        const v4i* q = static_cast<const v4i*>(p);
+        const v4i v = NT ? __builtin_nontemporal_load(q) : *q;
+        return make_uint4(v[0], v[1], v[2], v[3]);
     }
-    if (DT == MOE_DTYPE_F32) {
-        const uint32_t* p = static_cast<const uint32_t*>(base) + at;
-        if (VEC) {
-            const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    uint4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+
+// 8 values from base[at .. at + n): float32 bit patterns, 0 past n.  VEC: n is
+// 8 or at most 0, on a 16-byte boundary.
+template <int DT, bool VEC, bool NT>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int n, uint32_t (&v)[8]) {
+    if (VEC ? n > 0 : n >= 8) {
+        if (DT == MOE_DTYPE_F32) {
+            const uint32_t* p = static_cast<const uint32_t*>(base) + at;
+            const uint4 a = load16<VEC, NT>(p), b = load16<VEC, NT>(p + 4);
             v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0u;
-        }
-    } else {
-        const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-        if (VEC) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            const uint4 a = load16<VEC, NT>(static_cast<const uint16_t*>(base) + at);
             const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[2 * i] = w[i] << 16;
                 v[2 * i + 1] = w[i] & 0xFFFF0000u;
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < n ? (uint32_t)p[i] << 16 : 0u;
         }
+        return;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] = 0u;
+        if (!VEC && i < n)
+            v[i] = DT == MOE_DTYPE_F32 ? static_cast<const uint32_t*>(base)[at + i]
+                                       : (uint32_t)static_cast<const uint16_t*>(base)[at + i] << 16;
+    }
+}
+
+template <bool NT>
+__device__ __forceinline__ void store8(uint8_t* p, uint2 v) {
+    const v2i w = {(int)v.x, (int)v.y};
+    if (NT) __builtin_nontemporal_store(w, reinterpret_cast<v2i*>(p));
+    else *reinterpret_cast<v2i*>(p) = w;
 }
 
 __device__ __forceinline__ uint32_t abs_max(const uint32_t (&v)[8]) {
@@ -97,15 +112,17 @@ __device__ __forceinline__ uint2 pack8(const uint32_t (&v)[8], float inv) {
 // that each k-block's 32 scales leave as one 128-byte run.
 constexpr int kRowTile = 32, kColBlocks = 4;
 
-template <int DT, bool VEC>
+template <int DT, bool VEC, bool NT>
 __global__ __launch_bounds__(kThreads) void k_quantise_rows(const void* __restrict__ x, int64_t R, int C, int kb,
                                                             const int32_t* __restrict__ rows_used,
                                                             uint8_t* __restrict__ codes,
                                                             float* __restrict__ scales) {
     __shared__ float lds_s[kColBlocks][kRowTile];
     const int j = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-    const int64_t r0 = (int64_t)blockIdx.x * kRowTile;
-    const int kb0 = blockIdx.y * kColBlocks;
+    // column blocks first: the workgroups that run together read whole rows
+    const uint32_t across = (uint32_t)(kb + kColBlocks - 1) / kColBlocks;
+    const int64_t r0 = (int64_t)(blockIdx.x / across) * kRowTile;
+    const int kb0 = (int)(blockIdx.x % across) * kColBlocks;
     int64_t used = R;
     if (rows_used) {
         const int64_t n = *rows_used;
@@ -119,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void k_quantise_rows(const void* __restri
         const int b = kb0 + i % kColBlocks;
         const int64_t r = r0 + grp + kGroups * (i / kColBlocks);
         const int c = b * 128 + j * 8;
-        load8<DT, VEC>(x, r * C + c, r < used ? (C - c < 8 ? C - c : 8) : 0, v[i]);
+        load8<DT, VEC, NT>(x, r * C + c, r < used ? (C - c < 8 ? C - c : 8) : 0, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -128,7 +145,7 @@ __global__ __launch_bounds__(kThreads) void k_quantise_rows(const void* __restri
         const float s = block_scale(row_max(abs_max(v[i])));
         if (j == 0) lds_s[i % kColBlocks][rl] = s;
         if (r < used && b < kb)
-            *reinterpret_cast<uint2*>(codes + r * ((int64_t)kb * 128) + b * 128 + j * 8) = pack8(v[i], 1.f / s);
+            store8<NT>(codes + r * ((int64_t)kb * 128) + b * 128 + j * 8, pack8(v[i], 1.f / s));
     }
     __syncthreads();
     if (threadIdx.x < kRowTile * kColBlocks) {
@@ -146,7 +163,7 @@ __device__ __forceinline__ int t_word(int col, int word) {  // word = row / 4 of
     return col * 32 + ((word + col / 8 * 2) & 31);
 }
 
-template <int DT, bool VEC>
+template <int DT, bool VEC, bool NT>
 __global__ __launch_bounds__(kThreads) void k_quantise_weights(const void* __restrict__ w, int N, int K,
                                                                uint8_t* __restrict__ codes,
                                                                float* __restrict__ scales,
@@ -164,7 +181,7 @@ __global__ __launch_bounds__(kThreads) void k_quantise_weights(const void* __res
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int n = n0 + grp * 8 + i;
-        load8<DT, VEC>(w, (e * N + n) * (int64_t)K + c, n < N ? (K - c < 8 ? K - c : 8) : 0, v[i]);
+        load8<DT, VEC, NT>(w, (e * N + n) * (int64_t)K + c, n < N ? (K - c < 8 ? K - c : 8) : 0, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = umax2(m, abs_max(v[i]));
@@ -178,7 +195,7 @@ __global__ __launch_bounds__(kThreads) void k_quantise_weights(const void* __res
     for (int i = 0; i < 8; ++i) {
         const int n = n0 + grp * 8 + i;
         q[i] = pack8(v[i], inv);
-        if (n < N) *reinterpret_cast<uint2*>(codes + (e * N + n) * ((int64_t)kb * 128) + c) = q[i];
+        if (n < N) store8<NT>(codes + (e * N + n) * ((int64_t)kb * 128) + c, q[i]);
     }
     if (threadIdx.x == 0) scales[(e * nb + blockIdx.y) * kb + blockIdx.x] = s;
     if (!codes_t) return;
@@ -200,7 +217,7 @@ __global__ __launch_bounds__(kThreads) void k_quantise_weights(const void* __res
     for (int i = 0; i < 8; ++i) {  // transposed row grp + 16 i, bytes 8 j ..
         const int col = grp + kGroups * i, k = k0 + col;
         const uint2 o = make_uint2(lds_t[t_word(col, 2 * j)], lds_t[t_word(col, 2 * j + 1)]);
-        if (k < K) *reinterpret_cast<uint2*>(codes_t + (e * K + k) * ((int64_t)nb * 128) + n0 + j * 8) = o;
+        if (k < K) store8<NT>(codes_t + (e * K + k) * ((int64_t)nb * 128) + n0 + j * 8, o);
     }
 }
 
@@ -225,7 +242,7 @@ __device__ __forceinline__ uint32_t pow2_scale(uint32_t amax_bits, float& inv) {
     return (uint32_t)b;
 }
 
-template <int DT, bool VEC>
+template <int DT, bool VEC, bool NT>
 __global__ __launch_bounds__(kThreads) void k_quantise_columns(const void* __restrict__ x, int64_t R, int C, int E,
                                                                const int32_t* __restrict__ offsets, int64_t Rp,
                                                                uint8_t* __restrict__ codes,
@@ -235,7 +252,8 @@ __global__ __launch_bounds__(kThreads) void k_quantise_columns(const void* __res
     __shared__ int lds_wave[kThreads / kWave];
     __shared__ int lds_at[2];
     const int tid = threadIdx.x, j = tid % kLanes, grp = tid / kLanes;
-    const int64_t pb = blockIdx.x;  // padded row block
+    const uint32_t across = (uint32_t)(C + 127) / 128;  // column blocks first
+    const int64_t pb = blockIdx.x / across;             // padded row block
     int64_t lo = pb * 128, hi = R;
     if (offsets) {
         // blocks of experts 4 tid .. 4 tid + 3
@@ -276,12 +294,12 @@ __global__ __launch_bounds__(kThreads) void k_quantise_columns(const void* __res
         lo = lds_at[0];
         hi = lds_at[1];
     }
-    const int c0 = blockIdx.y * 128, c = c0 + j * 8;
+    const int c0 = (int)(blockIdx.x % across) * 128, c = c0 + j * 8;
     uint32_t v[8][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t r = lo + grp * 8 + i;
-        load8<DT, VEC>(x, r * C + c, r < hi ? (C - c < 8 ? C - c : 8) : 0, v[i]);
+        load8<DT, VEC, NT>(x, r * C + c, r < hi ? (C - c < 8 ? C - c : 8) : 0, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -315,28 +333,41 @@ __global__ __launch_bounds__(kThreads) void k_quantise_columns(const void* __res
     for (int i = 0; i < 8; ++i) {
         const int col = grp + kGroups * i;
         const uint2 o = make_uint2(lds_t[t_word(col, 2 * j)], lds_t[t_word(col, 2 * j + 1)]);
-        if (c0 + col < C) *reinterpret_cast<uint2*>(codes + (int64_t)(c0 + col) * Rp + pb * 128 + j * 8) = o;
+        if (c0 + col < C) store8<NT>(codes + (int64_t)(c0 + col) * Rp + pb * 128 + j * 8, o);
     }
 }
 
 // ---- host ---------------------------------------------------------------------------
 constexpr int32_t kMaxDim = 1 << 20;
-constexpr int64_t kMaxRows = int64_t(1) << 28;  // a launch holds fewer than 2^32 threads
+constexpr int64_t kMaxBlocks = int64_t(1) << 24;  // a launch holds fewer than 2^32 threads
+constexpr int64_t kMaxRows = int64_t(1) << 28;
 
 bool dtype_ok(int dt) { return dt == MOE_DTYPE_F32 || dt == MOE_DTYPE_BF16; }
 bool elem_aligned(const void* p, int dt) { return aligned(p, dt == MOE_DTYPE_F32 ? 4 : 2); }
 // whole 8-value vectors on 16-byte boundaries in every row
 bool vectors(const void* p, int cols) { return aligned(p, 16) && cols % 8 == 0; }
 
-// f(dtype, vectors) as compile-time constants
+// Inputs and outputs that together pass one and a half times the 256 MB
+// Infinity Cache go by it: little of them would be there for the next reader,
+// and a stream without the hint stays below 6.3 TB/s.  Measured without and
+// with it: rows 131072 x 2048 (805 MB) 154 and 135 us, weights 32 x 1536 x 2048
+// with their transpose (403 MB) 80 and 69; float32 rows 8192 x 7168 (294 MB) 44
+// and 53, columns 32768 x 2048 (201 MB) 38 and 43.
+constexpr int64_t kCacheBytes = int64_t(384) << 20;
+
+// f(dtype, vectors, non-temporal) as compile-time constants
 template <typename F>
-void with_input(int dt, bool vec, F f) {
+void with_input(int dt, bool vec, int64_t bytes, F f) {
     using std::integral_constant;
-    if (dt == MOE_DTYPE_F32 && vec) f(integral_constant<int, MOE_DTYPE_F32>(), integral_constant<bool, true>());
-    else if (dt == MOE_DTYPE_F32) f(integral_constant<int, MOE_DTYPE_F32>(), integral_constant<bool, false>());
-    else if (vec) f(integral_constant<int, MOE_DTYPE_BF16>(), integral_constant<bool, true>());
-    else f(integral_constant<int, MOE_DTYPE_BF16>(), integral_constant<bool, false>());
+    const auto with = [&](auto d) {
+        if (vec && bytes > kCacheBytes) f(d, std::true_type(), std::true_type());
+        else if (vec) f(d, std::true_type(), std::false_type());
+        else f(d, std::false_type(), std::false_type());
+    };
+    if (dt == MOE_DTYPE_F32) with(integral_constant<int, MOE_DTYPE_F32>());
+    else with(integral_constant<int, MOE_DTYPE_BF16>());
 }
+int64_t elem_bytes(int dt) { return dt == MOE_DTYPE_F32 ? 4 : 2; }
 
 }  // namespace
 }  // namespace moe
@@ -360,9 +391,11 @@ int moe_quantise_rows(int64_t R, int32_t C, int32_t dtype, const void* x, const 
         return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_DEVICE;
     const int kb = (C + 127) / 128;
-    const dim3 grid((unsigned)((R + kRowTile - 1) / kRowTile), (unsigned)((kb + kColBlocks - 1) / kColBlocks));
-    with_input(dtype, vectors(x, C), [&](auto dt, auto vec) {
-        hipLaunchKernelGGL((k_quantise_rows<decltype(dt)::value, decltype(vec)::value>), grid, dim3(kThreads), 0,
+    const int64_t blocks = (R + kRowTile - 1) / kRowTile * ((kb + kColBlocks - 1) / kColBlocks);
+    if (blocks >= kMaxBlocks) return MOE_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks);
+    with_input(dtype, vectors(x, C), R * C * (elem_bytes(dtype) + 1), [&](auto dt, auto vec, auto nt) {
+        hipLaunchKernelGGL((k_quantise_rows<decltype(dt)::value, decltype(vec)::value, decltype(nt)::value>), grid, dim3(kThreads), 0,
                            stream, x, R, C, kb, rows_used, codes, scales);
     });
     return launch_status();
@@ -378,8 +411,9 @@ int moe_quantise_weights(int32_t E, int32_t N, int32_t K, int32_t dtype, const v
         return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_DEVICE;
     const dim3 grid((unsigned)((K + 127) / 128), (unsigned)((N + 127) / 128), (unsigned)E);
-    with_input(dtype, vectors(w, K), [&](auto dt, auto vec) {
-        hipLaunchKernelGGL((k_quantise_weights<decltype(dt)::value, decltype(vec)::value>), grid, dim3(kThreads), 0,
+    const int64_t bytes = (int64_t)E * N * K * (elem_bytes(dtype) + (codes_t ? 2 : 1));
+    with_input(dtype, vectors(w, K), bytes, [&](auto dt, auto vec, auto nt) {
+        hipLaunchKernelGGL((k_quantise_weights<decltype(dt)::value, decltype(vec)::value, decltype(nt)::value>), grid, dim3(kThreads), 0,
                            stream, w, N, K, codes, scales, codes_t, scales_t);
     });
     return launch_status();
@@ -394,9 +428,11 @@ int moe_quantise_columns(int64_t R, int32_t C, int32_t E, int32_t dtype, const v
     if (!x || !codes || !scales) return MOE_ERR_INVALID_ARG;
     if (!elem_aligned(x, dtype) || !aligned(codes, 16) || !aligned(offsets, 4)) return MOE_ERR_INVALID_ARG;
     if (!device_ok()) return MOE_ERR_DEVICE;
-    const dim3 grid((unsigned)(Rp / 128), (unsigned)((C + 127) / 128));
-    with_input(dtype, vectors(x, C), [&](auto dt, auto vec) {
-        hipLaunchKernelGGL((k_quantise_columns<decltype(dt)::value, decltype(vec)::value>), grid, dim3(kThreads), 0,
+    const int64_t blocks = Rp / 128 * ((C + 127) / 128);
+    if (blocks >= kMaxBlocks) return MOE_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks);
+    with_input(dtype, vectors(x, C), R * C * (elem_bytes(dtype) + 1), [&](auto dt, auto vec, auto nt) {
+        hipLaunchKernelGGL((k_quantise_columns<decltype(dt)::value, decltype(vec)::value, decltype(nt)::value>), grid, dim3(kThreads), 0,
                            stream, x, R, C, E, offsets, Rp, codes, scales);
     });
     return launch_status();
