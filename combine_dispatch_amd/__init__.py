@@ -98,12 +98,15 @@ class MoeError(RuntimeError):
 
 
 _lib = None
+torch = None  # imported with the library, so that this module loads without it
 
 
 def lib():
     """Load libmoe_hip.so (built by combine_dispatch_amd/build.py)."""
-    global _lib
+    global _lib, torch
     if _lib is None:
+        import torch as _torch
+        torch = _torch
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing: build it with combine_dispatch_amd/build.py")
         L = ctypes.CDLL(LIB_PATH)
@@ -362,6 +365,11 @@ def _dense(what: str, name: str, t, shape: tuple, dtypes: tuple, device: int) ->
 
 
 def _gpu_of(what: str, t) -> int:
+    global _codes
+    if _lib is None:
+        lib()
+    if not _codes:
+        _codes = (torch.uint8, torch.float8_e4m3fn)
     device = t.get_device()
     if device < 0:
         raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: tensors must be on the GPU, got {t.device}")
@@ -370,7 +378,6 @@ def _gpu_of(what: str, t) -> int:
 
 def _call(what: str, fn, device: int, stream, *args) -> None:
     """The C entry with GPU `device` current, on `stream` or that GPU's current one."""
-    import torch
     if device != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _call(what, fn, device, stream, *args)
@@ -401,7 +408,6 @@ def moe_default_gate_options() -> MoeGateOptions:
 
 
 def _input_dtype(what: str, name: str, t) -> int:
-    import torch
     if t.dtype == torch.float32:
         return MOE_DTYPE_F32
     if t.dtype == torch.bfloat16:
@@ -411,7 +417,6 @@ def _input_dtype(what: str, name: str, t) -> int:
 
 def _gate_call(what, logits, opts, token_mask, K):
     """(GPU, shape, options, address of the logits, of the mask) of a router call."""
-    import torch
     device = _gpu_of(what, logits)
     _need(logits.dim() == 2, f"{what}: logits must be [T][E]")
     T, E = logits.shape
@@ -419,7 +424,7 @@ def _gate_call(what, logits, opts, token_mask, K):
     if opts is None:
         o = MoeGateOptions(dtype, MOE_SCORE_SOFTMAX, 1, 1.0)
     else:
-        o = MoeGateOptions(dtype, opts.score, opts.renormalise, opts.scale)
+        o = opts if opts.dtype == dtype else MoeGateOptions(dtype, opts.score, opts.renormalise, opts.scale)
     mask = None
     if token_mask is not None:
         mask = _dense(what, "token_mask", token_mask, (T,), (torch.uint8, torch.bool), device)
@@ -428,7 +433,6 @@ def _gate_call(what, logits, opts, token_mask, K):
 
 def _offsets(what, name, offsets, device):
     """(number of ranges, address) of an int32 array of range bounds; (1, None) for None."""
-    import torch
     if offsets is None:
         return 1, None
     n = offsets.shape[0] if offsets.dim() == 1 else 0
@@ -438,13 +442,12 @@ def _offsets(what, name, offsets, device):
 
 def moe_gate(logits, topk_idx, topk_w, bias=None, token_mask=None, opts=None, stream=None) -> None:
     """topk_idx (int64), topk_w (fp32) [T][K] <- the top-k gate of logits [T][E]."""
-    import torch
     what = "moe_gate"
     _need(topk_idx.dim() == 2, "moe_gate: topk_idx must be [T][K]")
     K = topk_idx.shape[1]
     device, shape, o, l, mask = _gate_call(what, logits, opts, token_mask, K)
     out = (logits.shape[0], K)
-    _call(what, lib().moe_gate, device, stream, shape, o, l,
+    _call(what, _lib.moe_gate, device, stream, shape, o, l,
           None if bias is None else _dense(what, "bias", bias, (logits.shape[1],), (torch.float32,), device), mask,
           _dense(what, "topk_idx", topk_idx, out, (torch.int64,), device),
           _dense(what, "topk_w", topk_w, out, (torch.float32,), device))
@@ -454,7 +457,6 @@ def moe_gate_backward(logits, dlogits, topk_idx=None, d_topk_w=None, slope=None,
                       token_mask=None, opts=None, stream=None) -> None:
     """dlogits [T][E] <- the gradient through topk_w (topk_idx, d_topk_w) and / or
     through the balance loss (slope of moe_balance_loss, d_loss [1] on the device)."""
-    import torch
     what = "moe_gate_backward"
     _need((topk_idx is None) == (d_topk_w is None), f"{what}: topk_idx and d_topk_w go together")
     _need((slope is None) == (d_loss is None), f"{what}: slope and d_loss go together")
@@ -469,7 +471,7 @@ def moe_gate_backward(logits, dlogits, topk_idx=None, d_topk_w=None, slope=None,
         S, off = _offsets(what, "seq_offsets", seq_offsets, device)
         balance = MoeBalanceGrad(_dense(what, "slope", slope, (S, E), (torch.float32,), device),
                                  _dense(what, "d_loss", d_loss, (1,), (torch.float32,), device), off, S)
-    _call(what, lib().moe_gate_backward, device, stream, shape, o, l, mask, idx, dw, balance,
+    _call(what, _lib.moe_gate_backward, device, stream, shape, o, l, mask, idx, dw, balance,
           _dense(what, "dlogits", dlogits, (T, E), (logits.dtype,), device))
 
 
@@ -481,14 +483,13 @@ def moe_balance_loss(logits, topk_idx, coef: float, loss, counts, slope, workspa
                      token_mask=None, opts=None, stream=None) -> None:
     """loss [1], counts (int32) and slope (fp32) [S][E] <- the balance loss of
     logits [T][E] with the choices topk_idx [T][K]."""
-    import torch
     what = "moe_balance_loss"
     _need(topk_idx.dim() == 2, f"{what}: topk_idx must be [T][K]")
     K = topk_idx.shape[1]
     device, shape, o, l, mask = _gate_call(what, logits, opts, token_mask, K)
     T, E = logits.shape
     S, off = _offsets(what, "seq_offsets", seq_offsets, device)
-    _call(what, lib().moe_balance_loss, device, stream, shape, o, l, mask,
+    _call(what, _lib.moe_balance_loss, device, stream, shape, o, l, mask,
           _dense(what, "topk_idx", topk_idx, (T, K), (torch.int64,), device), off, S, coef,
           _dense(what, "loss", loss, (1,), (torch.float32,), device),
           _dense(what, "counts", counts, (S, E), (torch.int32,), device),
@@ -501,34 +502,30 @@ def moe_padded_rows(R: int, E: int = 1) -> int:
     return int(lib().moe_padded_rows(R, E))
 
 
+_codes = ()  # the types of e4m3 codes, filled with the library
+
+
 def _up128(n: int) -> int:
     return (n + 127) // 128 * 128
 
 
-def _code_types():
-    import torch
-    return (torch.uint8, torch.float8_e4m3fn)
-
-
 def moe_quantise_rows(x, codes, scales, rows_used=None, stream=None) -> None:
     """codes [R][C'], scales fp32 [C'/128][R] <- x [R][C] (float32 or bfloat16)."""
-    import torch
     what = "moe_quantise_rows"
     device = _gpu_of(what, x)
     _need(x.dim() == 2, f"{what}: x must be [R][C]")
     R, C = x.shape
     Cp = _up128(C)
-    _call(what, lib().moe_quantise_rows, device, stream, R, C, _input_dtype(what, "x", x),
+    _call(what, _lib.moe_quantise_rows, device, stream, R, C, _input_dtype(what, "x", x),
           _dense(what, "x", x, (R, C), (x.dtype,), device),
           None if rows_used is None else _dense(what, "rows_used", rows_used, (1,), (torch.int32,), device),
-          _dense(what, "codes", codes, (R, Cp), _code_types(), device),
+          _dense(what, "codes", codes, (R, Cp), _codes, device),
           _dense(what, "scales", scales, (Cp // 128, R), (torch.float32,), device))
 
 
 def moe_quantise_weights(w, codes, scales, codes_t=None, scales_t=None, stream=None) -> None:
     """codes [E][N][K'], scales fp32 [E][N'/128][K'/128] <- w [E][N][K]; with
     codes_t [E][K][N'], scales_t [E][K'/128][N'/128] those of the transpose too."""
-    import torch
     what = "moe_quantise_weights"
     device = _gpu_of(what, w)
     _need(w.dim() == 3, f"{what}: w must be [E][N][K]")
@@ -537,32 +534,30 @@ def moe_quantise_weights(w, codes, scales, codes_t=None, scales_t=None, stream=N
     _need((codes_t is None) == (scales_t is None), f"{what}: codes_t and scales_t go together")
     ct = st = None
     if codes_t is not None:
-        ct = _dense(what, "codes_t", codes_t, (E, K, Np), _code_types(), device)
+        ct = _dense(what, "codes_t", codes_t, (E, K, Np), _codes, device)
         st = _dense(what, "scales_t", scales_t, (E, Kp // 128, Np // 128), (torch.float32,), device)
-    _call(what, lib().moe_quantise_weights, device, stream, E, N, K, _input_dtype(what, "w", w),
+    _call(what, _lib.moe_quantise_weights, device, stream, E, N, K, _input_dtype(what, "w", w),
           _dense(what, "w", w, (E, N, K), (w.dtype,), device),
-          _dense(what, "codes", codes, (E, N, Kp), _code_types(), device),
+          _dense(what, "codes", codes, (E, N, Kp), _codes, device),
           _dense(what, "scales", scales, (E, Np // 128, Kp // 128), (torch.float32,), device), ct, st)
 
 
 def moe_quantise_columns(x, codes, scales, offsets=None, stream=None) -> None:
     """codes [C][R'], UE8M0 scales [R'/128][C] <- x [R][C], R' = moe_padded_rows(R, E)."""
-    import torch
     what = "moe_quantise_columns"
     device = _gpu_of(what, x)
     _need(x.dim() == 2, f"{what}: x must be [R][C]")
     R, C = x.shape
     E, off = _offsets(what, "offsets", offsets, device)
     Rp = moe_padded_rows(R, E)
-    _call(what, lib().moe_quantise_columns, device, stream, R, C, E, _input_dtype(what, "x", x),
+    _call(what, _lib.moe_quantise_columns, device, stream, R, C, E, _input_dtype(what, "x", x),
           _dense(what, "x", x, (R, C), (x.dtype,), device), off,
-          _dense(what, "codes", codes, (C, Rp), _code_types(), device),
+          _dense(what, "codes", codes, (C, Rp), _codes, device),
           _dense(what, "scales", scales, (Rp // 128, C), (torch.uint8,), device))
 
 
 def moe_block_gemm(a, a_scales, w, w_scales, out, offsets=None, stream=None) -> None:
     """out [R][N] (bf16) <- the grouped product of the quantised rows a [R][K] and weights w [E][N][K]."""
-    import torch
     what = "moe_block_gemm"
     device = _gpu_of(what, a)
     _need(a.dim() == 2 and w.dim() == 3, f"{what}: a must be [R][K] and w [E][N][K]")
@@ -570,10 +565,10 @@ def moe_block_gemm(a, a_scales, w, w_scales, out, offsets=None, stream=None) -> 
     groups, off = _offsets(what, "offsets", offsets, device)
     if groups != E:
         raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: offsets must hold E + 1 = {E + 1} entries (none: E = 1)")
-    _call(what, lib().moe_block_gemm, device, stream, MoeBlockShape(R, N, K, E),
-          _dense(what, "a", a, (R, K), _code_types(), device),
+    _call(what, _lib.moe_block_gemm, device, stream, MoeBlockShape(R, N, K, E),
+          _dense(what, "a", a, (R, K), _codes, device),
           _dense(what, "a_scales", a_scales, (_up128(K) // 128, R), (torch.float32,), device),
-          _dense(what, "w", w, (E, N, K), _code_types(), device),
+          _dense(what, "w", w, (E, N, K), _codes, device),
           _dense(what, "w_scales", w_scales, (E, _up128(N) // 128, _up128(K) // 128), (torch.float32,), device), off,
           _dense(what, "out", out, (R, N), (torch.bfloat16, torch.int16), device))
 
@@ -581,16 +576,15 @@ def moe_block_gemm(a, a_scales, w, w_scales, out, offsets=None, stream=None) -> 
 def moe_block_gemm_wgrad(g, g_scales, x, x_scales, out, rows: int, offsets=None, stream=None) -> None:
     """out [E][N][K] (bf16) <- per group the product of the gradient's columns g [N][R'] and the input's x [K][R'];
     rows: R, the rows the columns layouts were made from."""
-    import torch
     what = "moe_block_gemm_wgrad"
     device = _gpu_of(what, g)
     _need(g.dim() == 2 and x.dim() == 2, f"{what}: g must be [N][R'] and x [K][R']")
     E, off = _offsets(what, "offsets", offsets, device)
     Rp = moe_padded_rows(rows, E)
     N, K = g.shape[0], x.shape[0]
-    _call(what, lib().moe_block_gemm_wgrad, device, stream, MoeBlockShape(rows, N, K, E),
-          _dense(what, "g", g, (N, Rp), _code_types(), device),
+    _call(what, _lib.moe_block_gemm_wgrad, device, stream, MoeBlockShape(rows, N, K, E),
+          _dense(what, "g", g, (N, Rp), _codes, device),
           _dense(what, "g_scales", g_scales, (Rp // 128, N), (torch.uint8,), device),
-          _dense(what, "x", x, (K, Rp), _code_types(), device),
+          _dense(what, "x", x, (K, Rp), _codes, device),
           _dense(what, "x_scales", x_scales, (Rp // 128, K), (torch.uint8,), device), off,
           _dense(what, "out", out, (E, N, K), (torch.bfloat16, torch.int16), device))

@@ -1,10 +1,10 @@
 // gate.hip -- the router's operators (include/moe_gate.h): top-k gate, its
 // gradient, the balance loss and its gradient.
 //
-// All kernels give one token row to 16 lanes (a DPP row): lane j keeps
-// VPL = ceil(E / 16) logits in registers, so four rows run in a wave and every
-// cross-lane step is four DPP rotations inside the row, with no LDS and no
-// barrier.  What bounds them: at training sizes one read of the logits (and
+// All kernels give one token row to L lanes: lane j keeps VPL = ceil(E / L)
+// logits in registers.  L = 16 (a DPP row): four rows run in a wave and every
+// cross-lane step is four DPP rotations, with no LDS and no barrier.  L = 64
+// (the gate of few tokens): a wave per row, two permlane swaps more.  What bounds them: at training sizes one read of the logits (and
 // one write of the gradient) against HBM; at decode sizes the launch and the
 // chain of K dependent selections.
 #include "../../include/moe_gate.h"
@@ -17,7 +17,7 @@ namespace {
 constexpr int kRowLanes = 16;
 constexpr int kThreads = 256;
 constexpr int kRowsPerBlock = kThreads / kRowLanes;
-constexpr int kMaxSlots = 4;  // slots per lane: K <= 64
+constexpr int kMaxSlots = 4;  // slots per lane of 16: K <= 64
 
 // ---- steps across the 16 lanes of a row ------------------------------------
 template <int N>
@@ -30,39 +30,59 @@ __device__ __forceinline__ float ror(float v) {
 }
 __device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint32_t umin2(uint32_t a, uint32_t b) { return a < b ? a : b; }
+// The other halves of 32 and of 64 lanes, for every lane: f(v, other).
+template <typename F>
+__device__ __forceinline__ uint32_t across_rows(uint32_t v, F f) {
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = f(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return f(b[0], b[1]);
+}
+template <int L = kRowLanes>
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
     v = umax2(v, ror<8>(v));
     v = umax2(v, ror<4>(v));
     v = umax2(v, ror<2>(v));
-    return umax2(v, ror<1>(v));
+    v = umax2(v, ror<1>(v));
+    return L == 16 ? v : across_rows(v, umax2);
 }
+template <int L = kRowLanes>
 __device__ __forceinline__ uint32_t row_min(uint32_t v) {
     v = umin2(v, ror<8>(v));
     v = umin2(v, ror<4>(v));
     v = umin2(v, ror<2>(v));
-    return umin2(v, ror<1>(v));
+    v = umin2(v, ror<1>(v));
+    return L == 16 ? v : across_rows(v, umin2);
 }
+template <int L = kRowLanes>
 __device__ __forceinline__ float row_max(float v) {
     v = fmaxf(v, ror<8>(v));
     v = fmaxf(v, ror<4>(v));
     v = fmaxf(v, ror<2>(v));
-    return fmaxf(v, ror<1>(v));
+    v = fmaxf(v, ror<1>(v));
+    return L == 16 ? v : __uint_as_float(across_rows(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
 }
 // The same bits in every lane: each step adds the same two values in one of
 // the two orders.
+template <int L = kRowLanes>
 __device__ __forceinline__ float row_sum(float v) {
     v += ror<8>(v);
     v += ror<4>(v);
     v += ror<2>(v);
-    return v + ror<1>(v);
+    v += ror<1>(v);
+    return L == 16 ? v : __uint_as_float(across_rows(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
 }
 
 // ---- a row's logits ----------------------------------------------------------
-// Lane j's value i is expert ((i / VEC) * 16 + j) * VEC + i % VEC: VEC wide
+// Lane j's value i is expert ((i / VEC) * L + j) * VEC + i % VEC: VEC wide
 // loads, ascending in i.  Experts past E read as -inf.
-template <int VEC>
+template <int VEC, int L = kRowLanes>
 __device__ __forceinline__ int expert_of(int i, int j) {
-    return ((i / VEC) * kRowLanes + j) * VEC + i % VEC;
+    return ((i / VEC) * L + j) * VEC + i % VEC;
 }
 
 template <int DT>
@@ -85,12 +105,12 @@ struct alignas(sizeof(T) * VEC) Pack {
     T v[VEC];
 };
 
-template <int DT, int VPL, int VEC>
+template <int DT, int VPL, int VEC, int L = kRowLanes>
 __device__ __forceinline__ void load_row(const typename Elem<DT>::type* row, int E, int j, float (&v)[VPL]) {
     typedef Pack<typename Elem<DT>::type, VEC> P;
 #pragma unroll
     for (int i = 0; i < VPL; i += VEC) {
-        const int e = expert_of<VEC>(i, j);
+        const int e = expert_of<VEC, L>(i, j);
         if (e < E) {  // E % VEC == 0: all or none
             const P p = *reinterpret_cast<const P*>(row + e);
 #pragma unroll
@@ -128,9 +148,6 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t k = b ^ ((int32_t)b < 0 ? 0xFFFFFFFFu : 0x80000000u);
     return v == -INFINITY ? 0u : k;
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float(k ^ ((int32_t)k < 0 ? 0x80000000u : 0xFFFFFFFFu));
-}
 __device__ __forceinline__ uint64_t order_key64(double v) {
     if (v != v) return ~0ull;
     const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
@@ -139,29 +156,63 @@ __device__ __forceinline__ uint64_t order_key64(double v) {
 }
 
 // ---- top-k gate --------------------------------------------------------------
-// K rounds of: the lane's largest key, the row's largest (4 DPP steps), the
-// lowest expert holding it (4 more), taken out.  Without a bias the key is the
-// logit itself, so the choice is exact.  With a bias the key is
-// sigmoid + bias: float32 first, and where two neighbours among the first
-// K + 1 lie within kNear of each other (a few tokens in a thousand) the row is
-// chosen again by float64 keys.  kNear: the float32 key is off by at most
-// 2^-22 (exp and division: 4 half-steps of a value below 1) plus half a step
-// of the sum, 2^-24 (1 + |key|); two keys' errors are below
-// 2^-20 (1 + |key|).
-template <int DT, int VPL, int VEC, bool BIAS>
+// K rounds of: the lane's largest key, the row's largest, taken out.  The low
+// B bits of a 32-bit key hold the expert (the lower one larger), so keys are
+// unique, a round needs no search for the winner's place, and equal values go
+// to the lower expert by themselves.  The bits above hold
+//   bf16 logits      the logit itself, exactly (16 bits): nothing left to do
+//   float32 logits   the logit without its last B bits
+//   sigmoid + bias   (s + 2) in 30 - B fractional bits, s clamped to [-2, 2]
+// In the last two cases one round more tells whether any two neighbours among
+// the first K + 1 are too close for that (a few rows in a thousand).  Such a
+// row's candidates, and those that follow closely behind them, are put in order
+// by their full keys: the float32 logit, or sigmoid + bias in float64; if they
+// are more than L, all its experts are chosen again by their full keys.  How close: equal float32 keys; for the bias the key's errors,
+// twice 2^-22 for exp2, its argument and the reciprocal (s (1 - s) |l| is below
+// 0.23, so the argument's rounding weighs less than half a step), 2^-24 (1 + |b|)
+// for the sum and 2^-23 for s + 2, in all below 3.25 * 2^-20, in units of
+// 2^(B - 30), and one unit more for the cut.
+template <int DT, bool BIAS, int B>
+__device__ __forceinline__ uint32_t packed_key(float v, float bias, int e) {
+    constexpr uint32_t kMask = (1u << B) - 1;
+    uint32_t k;
+    if (BIAS) {
+        if (v == -INFINITY || bias == -INFINITY) return 0;
+        const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -0x1.715476p+0f)) + bias;
+        const float c = s != s ? 2.f : fminf(fmaxf(s, -2.f), 2.f);
+        // 1 .. 2^(32 - B) - 1
+        k = (uint32_t)fminf(fmaxf((c + 2.f) * (float)(1u << (30 - B)), 1.f), (float)((1u << (32 - B)) - 256u)) << B;
+    } else {
+        k = order_key(v);
+        if (k == 0) return 0;
+        k &= ~kMask;
+    }
+    return k | (kMask - (uint32_t)e);
+}
+template <bool BIAS, int B>
+__device__ __forceinline__ bool too_close(uint32_t above, uint32_t below) {
+    constexpr uint32_t kUnits = BIAS ? (uint32_t)(3.25f * (float)(1 << (B < 10 ? 10 - B : 0))) + 2u : 0u;
+    return below != 0 && (above >> B) - (below >> B) <= kUnits;
+}
+constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
+
+template <int DT, int VPL, int VEC, bool BIAS, int L>
 __global__ __launch_bounds__(kThreads) void k_gate(const typename Elem<DT>::type* __restrict__ logits,
                                                    const float* __restrict__ bias,
                                                    const uint8_t* __restrict__ mask, int T, int E, int K,
                                                    int score, int renorm, float scale,
                                                    int64_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
-    const int j = threadIdx.x & (kRowLanes - 1);
-    const int64_t t = (int64_t)blockIdx.x * kRowsPerBlock + threadIdx.x / kRowLanes;
+    constexpr int kB = log2_of(L * VPL);      // bits of an expert
+    constexpr int kSlots = 64 / L;            // slots per lane
+    constexpr bool kCheck = BIAS || DT == MOE_DTYPE_F32;
+    const int j = threadIdx.x & (L - 1);
+    const int64_t t = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
     if (t >= T) return;  // whole rows of lanes leave together
     const typename Elem<DT>::type* row = logits + t * E;
     int64_t* idx_out = topk_idx + t * K;
     float* w_out = topk_w + t * K;
     if (mask && !mask[t]) {
-        for (int k = j; k < K; k += kRowLanes) {
+        for (int k = j; k < K; k += L) {
             idx_out[k] = -1;
             w_out[k] = 0.f;
         }
@@ -172,114 +223,162 @@ __global__ __launch_bounds__(kThreads) void k_gate(const typename Elem<DT>::type
     float top = 0.f, total = 1.f;  // softmax over all experts: largest logit, sum of exp
     {
         float v[VPL];
-        load_row<DT, VPL, VEC>(row, E, j, v);
+        load_row<DT, VPL, VEC, L>(row, E, j, v);
+        float add[VPL];
+        if (BIAS) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const int e = expert_of<VEC, L>(i, j);
+                add[i] = e < E ? bias[e] : 0.f;
+            }
+        }
         if (score == MOE_SCORE_SOFTMAX && !renorm) {
             top = v[0];
 #pragma unroll
             for (int i = 1; i < VPL; ++i) top = fmaxf(top, v[i]);
-            top = row_max(top);
+            top = row_max<L>(top);
             total = 0.f;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) total += expf(v[i] - top);
-            total = row_sum(total);
+            total = row_sum<L>(total);
         }
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            float s = v[i];
-            if (BIAS) {
-                const int e = expert_of<VEC>(i, j);
-                s = v[i] == -INFINITY ? v[i] : sigmoid(v[i]) + (e < E ? bias[e] : 0.f);
-            }
-            key[i] = order_key(s);
-        }
+        for (int i = 0; i < VPL; ++i)
+            key[i] = packed_key<DT, BIAS, kB>(v[i], BIAS ? add[i] : 0.f, expert_of<VEC, L>(i, j));
     }
 
-    int sel[kMaxSlots] = {-1, -1, -1, -1};
-    bool near = false;
-    float last = 0.f;
-    const int rounds = BIAS && K < E ? K + 1 : K;
+    int sel[kSlots];
 #pragma unroll
-    for (int b = 0; b <= kMaxSlots; ++b) {  // the fifth: only the extra round of K = 64
+    for (int b = 0; b < kSlots; ++b) sel[b] = -1;
+    // takes out the largest key
+    const auto next = [&]() {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) m = umax2(m, key[i]);
+        m = row_max<L>(m);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = key[i] == m ? 0u : key[i];
+        return m;
+    };
+    const auto expert = [](uint32_t m) { return m ? (int)(((1u << kB) - 1) & ~m) : -1; };
+    bool close = false, edge = false;  // any two neighbours; the last two
+    uint32_t last = 0xFFFFFFFFu;
+    const int rounds = kCheck && K < E ? K + 1 : K;
+#pragma unroll
+    for (int b = 0; b <= kSlots; ++b) {  // the last: only the extra round of K = 64
 #pragma unroll 1
-        for (int k = b * kRowLanes; k < rounds && k < (b + 1) * kRowLanes; ++k) {
-            uint32_t m = key[0];
-#pragma unroll
-            for (int i = 1; i < VPL; ++i) m = umax2(m, key[i]);
-            m = row_max(m);
-            if (BIAS) {
-                const float s = key_value(m);
-                near |= k > 0 && m != 0 && last - s <= 0x1p-20f * (1.f + fabsf(s));
-                last = s;
-                if (k == K) break;
+        for (int k = b * L; k < rounds && k < (b + 1) * L; ++k) {
+            const uint32_t m = next();
+            if (kCheck) {
+                edge = k > 0 && too_close<BIAS, kB>(last, m);
+                close |= edge;
+                last = m;
             }
-            uint32_t at = 0x7FFFFFFFu;
-#pragma unroll
-            for (int i = VPL - 1; i >= 0; --i) at = key[i] == m ? (uint32_t)expert_of<VEC>(i, j) : at;
-            at = row_min(at);
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) key[i] = expert_of<VEC>(i, j) == (int)at ? 0u : key[i];
-            if (b < kMaxSlots && (k & (kRowLanes - 1)) == j) sel[b < kMaxSlots ? b : 0] = m ? (int)at : -1;
+            if (b < kSlots && (k & (L - 1)) == j) sel[b < kSlots ? b : 0] = expert(m);
         }
     }
 
-    if (BIAS && near) {
+    if (kCheck && close && K < L) {
+        // Candidates one per lane: those chosen, and behind them as many as
+        // follow closely; put in order by their full keys.
+        int n = rounds;
+        edge = edge && rounds > K;
+        while (edge && n < L && n < E) {
+            const uint32_t m = next();
+            edge = too_close<BIAS, kB>(last, m);
+            last = m;
+            if (j == n) sel[0] = expert(m);
+            ++n;
+        }
+        if (!edge || n == E) {
+            const int mine = j < n ? sel[0] : -1;
+            uint64_t full = 0;
+            if (mine >= 0) {
+                const float v = Elem<DT>::get(row[mine]);
+                full = BIAS ? order_key64(sigmoid64(v) + (double)bias[mine]) : (uint64_t)order_key(v);
+            }
+            int rank = 0;
+            for (int i = 0; i < n; ++i) {
+                uint64_t other = (uint32_t)__shfl((int)(uint32_t)full, i, L);
+                if (BIAS) other |= (uint64_t)(uint32_t)__shfl((int)(full >> 32), i, L) << 32;
+                const int e = __shfl(mine, i, L);
+                rank += other > full || (other == full && (e < mine || (e == mine && i < j)));
+            }
+            // to the lane of its rank
+            const int base = (int)(threadIdx.x & (kWave - 1)) - j;
+            const int moved = __builtin_amdgcn_ds_permute(4 * (base + (j < n ? rank : j)), mine);
+            sel[0] = j < n ? moved : -1;
+            close = false;
+        }
+    }
+
+    if (kCheck && close) {
         uint32_t hi[VPL], lo[VPL];
         float v[VPL];
-        load_row<DT, VPL, VEC>(row, E, j, v);
+        load_row<DT, VPL, VEC, L>(row, E, j, v);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const int e = expert_of<VEC>(i, j);
-            const uint64_t k64 = v[i] == -INFINITY ? 0ull : order_key64(sigmoid64(v[i]) + (double)(e < E ? bias[e] : 0.f));
-            hi[i] = (uint32_t)(k64 >> 32);
-            lo[i] = (uint32_t)k64;
+            if (BIAS) {
+                const int e = expert_of<VEC, L>(i, j);
+                const uint64_t k64 =
+                    v[i] == -INFINITY ? 0ull : order_key64(sigmoid64(v[i]) + (double)(e < E ? bias[e] : 0.f));
+                hi[i] = (uint32_t)(k64 >> 32);
+                lo[i] = (uint32_t)k64;
+            } else {
+                hi[i] = order_key(v[i]);
+                lo[i] = 0;
+            }
         }
 #pragma unroll
-        for (int b = 0; b < kMaxSlots; ++b) {
+        for (int b = 0; b < kSlots; ++b) {
 #pragma unroll 1
-            for (int k = b * kRowLanes; k < K && k < (b + 1) * kRowLanes; ++k) {
+            for (int k = b * L; k < K && k < (b + 1) * L; ++k) {
                 uint32_t mh = hi[0];
 #pragma unroll
                 for (int i = 1; i < VPL; ++i) mh = umax2(mh, hi[i]);
-                mh = row_max(mh);
+                mh = row_max<L>(mh);
                 uint32_t ml = 0;
+                if (BIAS) {
 #pragma unroll
-                for (int i = 0; i < VPL; ++i) ml = umax2(ml, hi[i] == mh ? lo[i] : 0u);
-                ml = row_max(ml);
+                    for (int i = 0; i < VPL; ++i) ml = umax2(ml, hi[i] == mh ? lo[i] : 0u);
+                    ml = row_max<L>(ml);
+                }
                 uint32_t at = 0x7FFFFFFFu;
 #pragma unroll
                 for (int i = VPL - 1; i >= 0; --i)
-                    at = hi[i] == mh && lo[i] == ml ? (uint32_t)expert_of<VEC>(i, j) : at;
-                at = row_min(at);
+                    at = hi[i] == mh && lo[i] == ml ? (uint32_t)expert_of<VEC, L>(i, j) : at;
+                at = row_min<L>(at);
 #pragma unroll
                 for (int i = 0; i < VPL; ++i) {
-                    const bool gone = expert_of<VEC>(i, j) == (int)at;
+                    const bool gone = expert_of<VEC, L>(i, j) == (int)at;
                     hi[i] = gone ? 0u : hi[i];
                     lo[i] = gone ? 0u : lo[i];
                 }
-                if ((k & (kRowLanes - 1)) == j) sel[b] = (mh | ml) ? (int)at : -1;
+                if ((k & (L - 1)) == j) sel[b] = (mh | ml) ? (int)at : -1;
             }
         }
     }
 
-    // weights of the chosen: lane j holds slots j, j + 16, ...
-    float s[kMaxSlots];
+    // weights of the chosen: lane j holds slots j, j + L, ...
+    float s[kSlots];
     float chosen_top = -INFINITY;
 #pragma unroll
-    for (int b = 0; b < kMaxSlots; ++b) {
+    for (int b = 0; b < kSlots; ++b) {
+        if (b * L + j >= K) sel[b] = -1;  // candidates that were not chosen
         s[b] = sel[b] >= 0 ? Elem<DT>::get(row[sel[b]]) : -INFINITY;
         chosen_top = fmaxf(chosen_top, s[b]);
     }
-    if (score == MOE_SCORE_SOFTMAX && renorm) top = row_max(chosen_top);
+    if (score == MOE_SCORE_SOFTMAX && renorm) top = row_max<L>(chosen_top);
     float sum = 0.f;
 #pragma unroll
-    for (int b = 0; b < kMaxSlots; ++b) {
+    for (int b = 0; b < kSlots; ++b) {
         s[b] = sel[b] < 0 ? 0.f : score == MOE_SCORE_SIGMOID ? sigmoid(s[b]) : expf(s[b] - top);
         sum += s[b];
     }
-    if (renorm) total = row_sum(sum);
+    if (renorm) total = row_sum<L>(sum);
 #pragma unroll
-    for (int b = 0; b < kMaxSlots; ++b) {
-        const int k = b * kRowLanes + j;
+    for (int b = 0; b < kSlots; ++b) {
+        const int k = b * L + j;
         if (k < K) {
             const float w = total == 0.f ? 0.f : s[b] / total;
             idx_out[k] = sel[b];
@@ -477,7 +576,7 @@ __global__ __launch_bounds__(kThreads) void k_gate_backward(
 // k_balance_final: blocks over (sequence, 16 experts) add the rows; the last
 // block to finish adds the blocks' losses in a fixed order.
 constexpr int kChunk = 32;
-constexpr int kFinalThreads = 512;
+constexpr int kFinalThreads = 1024;
 constexpr int kFinalBlocks = 512;
 constexpr int kFinalExperts = 16;
 
@@ -496,6 +595,8 @@ __global__ __launch_bounds__(kThreads) void k_balance_part(
     int S, BalanceWs ws) {
     extern __shared__ float lds_sum[];  // [4][E] probability sums, then [E] counts
     __shared__ int lds_n[2];
+    __shared__ int lds_off[kThreads + 1];  // the sequences' bounds, if there are at most kThreads
+    constexpr int kRows = kChunk / kRowsPerBlock, kSlots = kChunk * 64 / kThreads;
     int* lds_c = reinterpret_cast<int*>(lds_sum + 4 * E);
     const int tid = threadIdx.x, j = tid & (kRowLanes - 1), wave = tid / kWave;
     const int b = blockIdx.x;
@@ -504,9 +605,66 @@ __global__ __launch_bounds__(kThreads) void k_balance_part(
     if (t0 >= T) return;  // T == 0
     const bool soft = score == MOE_SCORE_SOFTMAX;
 
-    for (int q = seq_offsets ? sequence_of(seq_offsets, S, t0, j) : 0; q < S; ++q) {
+    // everything of the chunk's tokens, before it is known whose they are: a
+    // lane group's rows as probabilities (0 for padding), a thread's slots
+    float p[kRows][VPL];
+    bool live[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const int t = t0 + tid / kRowLanes + r * kRowsPerBlock;
+        live[r] = t < t1 && !(mask && !mask[t]);
+        if (live[r]) {
+            load_row<DT, VPL, VEC>(logits + (int64_t)t * E, E, j, p[r]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) p[r][i] = -INFINITY;
+        }
+    }
+    int chosen[kSlots];
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        const int at = tid + i * kThreads;
+        chosen[i] = -1;
+        if (at < (t1 - t0) * K) {
+            const int64_t e = topk_idx[(int64_t)t0 * K + at];
+            if (e >= 0 && e < E && !(mask && !mask[t0 + at / K])) chosen[i] = (int)e;
+        }
+    }
+    const int32_t* off = seq_offsets;
+    int q = 0;
+    if (seq_offsets && S <= kThreads) {
+        const int32_t end = tid < S ? seq_offsets[tid + 1] : 0;
+        if (tid < S) lds_off[tid + 1] = end;
+        if (tid == 0) lds_off[0] = seq_offsets[0];
+        q = __syncthreads_count(tid < S && end <= t0);  // sequences that end before the chunk
+        off = lds_off;
+    } else if (seq_offsets) {
+        q = sequence_of(seq_offsets, S, t0, j);
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        float top = 0.f, total = 0.f;
+        if (soft) {
+            top = p[r][0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) top = fmaxf(top, p[r][i]);
+            top = row_max(top);
+            top = top == -INFINITY ? 0.f : top;
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            p[r][i] = soft ? expf(p[r][i] - top) : sigmoid(p[r][i]);
+            total += p[r][i];
+        }
+        total = row_sum(total);
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) p[r][i] *= inv;
+    }
+
+    for (; q < S; ++q) {
         int lo, hi;
-        sequence_range(seq_offsets, q, T, lo, hi);
+        sequence_range(off, q, T, lo, hi);
         if (lo >= t1) break;
         lo = lo < t0 ? t0 : lo;
         hi = hi < t1 ? hi : t1;
@@ -516,44 +674,29 @@ __global__ __launch_bounds__(kThreads) void k_balance_part(
         if (tid < 2) lds_n[tid] = 0;
         __syncthreads();
         int found = 0;
-        for (int i = tid; i < (hi - lo) * K; i += kThreads) {
-            const int t = lo + i / K;
-            const int64_t e = topk_idx[(int64_t)lo * K + i];
-            if (e >= 0 && e < E && !(mask && !mask[t])) {
-                atomicAdd(&lds_c[e], 1);
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            const int at = tid + i * kThreads;
+            if (chosen[i] >= 0 && at >= (lo - t0) * K && at < (hi - t0) * K) {
+                atomicAdd(&lds_c[chosen[i]], 1);
                 ++found;
             }
         }
         if (found) atomicAdd(&lds_n[1], found);
         float acc[VPL];
+        bool in[kRows];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
-        for (int t = lo + tid / kRowLanes; t < hi; t += kRowsPerBlock) {
-            if (mask && !mask[t]) continue;
-            if (j == 0) atomicAdd(&lds_n[0], 1);
-            float v[VPL];
-            load_row<DT, VPL, VEC>(logits + (int64_t)t * E, E, j, v);
-            float top = 0.f, total = 0.f;
-            if (soft) {
-                top = v[0];
-#pragma unroll
-                for (int i = 1; i < VPL; ++i) top = fmaxf(top, v[i]);
-                top = row_max(top);
-                top = top == -INFINITY ? 0.f : top;
-            }
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                v[i] = soft ? expf(v[i] - top) : sigmoid(v[i]);
-                total += v[i];
-            }
-            total = row_sum(total);
-            const float inv = total == 0.f ? 0.f : 1.f / total;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) acc[i] += v[i] * inv;
+        for (int r = 0; r < kRows; ++r) {
+            const int t = t0 + tid / kRowLanes + r * kRowsPerBlock;
+            in[r] = live[r] && t >= lo && t < hi;
+            if (in[r] && j == 0) atomicAdd(&lds_n[0], 1);
         }
         // the wave's four rows, then the block's four waves
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
+            acc[i] = 0.f;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) acc[i] += in[r] ? p[r][i] : 0.f;
             acc[i] += __shfl_xor(acc[i], 16);
             acc[i] += __shfl_xor(acc[i], 32);
             const int e = expert_of<VEC>(i, j);
@@ -574,71 +717,91 @@ __global__ __launch_bounds__(kFinalThreads) void k_balance_final(int T, int E, c
                                                                  int32_t* __restrict__ counts,
                                                                  float* __restrict__ slope, BalanceWs ws,
                                                                  int lanes_per_seq) {
-    constexpr int kSlices = kFinalThreads / kFinalExperts;
+    // The first half of the threads adds up work items; the second finds the
+    // number of sequences with a live token meanwhile.
+    constexpr int kHalf = kFinalThreads / 2, kSlices = kHalf / kFinalExperts;
     __shared__ double lds_p[kSlices][kFinalExperts];
     __shared__ int lds_c[kSlices][kFinalExperts];
-    __shared__ int lds_live;
+    __shared__ int lds_live[kHalf / kWave];
     __shared__ int2 lds_nc;
     __shared__ bool lds_last;
     const int tid = threadIdx.x;
-    if (tid == 0) lds_live = 0;
-    __syncthreads();
-    // sequences with a live token: lanes_per_seq lanes (a power of two) each
-    {
-        int found = 0;
-        const int per = kFinalThreads / lanes_per_seq, ln = tid % lanes_per_seq;
-        for (int q0 = 0; q0 < S; q0 += per) {
-            const int q = q0 + tid / lanes_per_seq;
-            int n = 0;
-            if (q < S) {
-                int lo, hi;
-                sequence_range(seq_offsets, q, T, lo, hi);
-                if (lo < hi)
-                    for (int b = lo / kChunk + ln; b <= (hi - 1) / kChunk; b += lanes_per_seq) n += ws.pair_n[b + q].x;
-            }
-            for (int m = 1; m < lanes_per_seq; m <<= 1) n += __shfl_xor(n, m);
-            found += ln == 0 && n > 0;
-        }
-        if (found) atomicAdd(&lds_live, found);
-    }
-    __syncthreads();
-    const int live = lds_live;
-
     double sum = 0.0;  // this block's share of the loss (thread 0)
+    int live = 0;
     const int eblocks = (E + kFinalExperts - 1) / kFinalExperts;
     const int64_t items = (int64_t)S * eblocks;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int q = (int)(it / eblocks), e = (int)(it % eblocks) * kFinalExperts + tid % kFinalExperts;
         const int sl = tid / kFinalExperts;
-        int lo, hi;
-        sequence_range(seq_offsets, q, T, lo, hi);
-        const int b0 = lo / kChunk, b1 = lo < hi ? (hi - 1) / kChunk : b0 - 1;
-        double p = 0.0;
-        int c = 0;
-        if (e < E)
-            for (int b = b0 + sl; b <= b1; b += kSlices) {
-                p += (double)ws.part_p[(int64_t)(b + q) * E + e];
-                c += ws.part_c[(int64_t)(b + q) * E + e];
+        if (tid < kHalf) {
+            int lo, hi;
+            sequence_range(seq_offsets, q, T, lo, hi);
+            const int b0 = lo / kChunk, b1 = lo < hi ? (hi - 1) / kChunk : b0 - 1;
+            double p = 0.0;
+            int c = 0;
+            if (e < E)
+                for (int b = b0 + sl; b <= b1; b += 8 * kSlices) {  // eight rows' loads in flight
+                    float pv[8];
+                    int cv[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const bool in = b + u * kSlices <= b1;
+                        const int64_t at = (int64_t)(in ? b + u * kSlices + q : b + q) * E + e;
+                        pv[u] = ws.part_p[at];
+                        cv[u] = ws.part_c[at];
+                        if (!in) pv[u] = 0.f, cv[u] = 0;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        p += (double)pv[u];
+                        c += cv[u];
+                    }
+                }
+            lds_p[sl][tid % kFinalExperts] = p;
+            lds_c[sl][tid % kFinalExperts] = c;
+        } else {
+            if (tid < kHalf + kWave) {  // live tokens and counted slots of this sequence
+                int lo, hi, n = 0, m = 0;
+                sequence_range(seq_offsets, q, T, lo, hi);
+                if (lo < hi)
+                    for (int b = lo / kChunk + tid - kHalf; b <= (hi - 1) / kChunk; b += kWave) {
+                        const int2 v = ws.pair_n[b + q];
+                        n += v.x;
+                        m += v.y;
+                    }
+                for (int x = 1; x < kWave; x <<= 1) {
+                    n += __shfl_xor(n, x);
+                    m += __shfl_xor(m, x);
+                }
+                if (tid == kHalf) lds_nc = make_int2(n, m);
             }
-        lds_p[sl][tid % kFinalExperts] = p;
-        lds_c[sl][tid % kFinalExperts] = c;
-        if (tid < kWave) {
-            int n = 0, m = 0;
-            for (int b = b0 + tid; b <= b1; b += kWave) {
-                const int2 v = ws.pair_n[b + q];
-                n += v.x;
-                m += v.y;
+            if (it == blockIdx.x) {  // once: lanes_per_seq lanes (a power of two) a sequence
+                int found = 0;
+                const int per = kHalf / lanes_per_seq, ln = tid % lanes_per_seq;
+                for (int s0 = 0; s0 < S; s0 += per) {
+                    const int s = s0 + (tid - kHalf) / lanes_per_seq;
+                    int n = 0;
+                    if (s < S) {
+                        int lo, hi;
+                        sequence_range(seq_offsets, s, T, lo, hi);
+                        if (lo < hi)
+                            for (int b = lo / kChunk + ln; b <= (hi - 1) / kChunk; b += lanes_per_seq)
+                                n += ws.pair_n[b + s].x;
+                    }
+                    for (int m = 1; m < lanes_per_seq; m <<= 1) n += __shfl_xor(n, m);
+                    found += ln == 0 && n > 0;
+                }
+                for (int x = 1; x < kWave; x <<= 1) found += __shfl_xor(found, x);
+                if (tid % kWave == 0) lds_live[(tid - kHalf) / kWave] = found;
             }
-            for (int x = 1; x < kWave; x <<= 1) {
-                n += __shfl_xor(n, x);
-                m += __shfl_xor(m, x);
-            }
-            if (tid == 0) lds_nc = make_int2(n, m);
         }
         __syncthreads();
         if (tid < kFinalExperts) {
-            p = 0.0;
-            c = 0;
+            live = 0;
+            for (int i = 0; i < kHalf / kWave; ++i) live += lds_live[i];
+            double p = 0.0;
+            int c = 0;
+#pragma unroll
             for (int i = 0; i < kSlices; ++i) {
                 p += lds_p[i][tid];
                 c += lds_c[i][tid];
@@ -678,7 +841,7 @@ bool gate_shape_ok(const moe_gate_shape_t* s) {
     return s && s->T >= 0 && s->T <= kMaxTokens && s->E >= 1 && s->E <= 1024 && s->K >= 1 && s->K <= 64 && s->K <= s->E;
 }
 
-// 16 * VPL >= E, VPL a power of two; VEC as wide as 16 bytes where every row
+// L * VPL >= E, VPL a power of two; VEC as wide as 16 bytes where every row
 // starts on such a boundary and holds whole vectors, else single values.
 template <int DT, int VPL, typename F>
 void with_vec(int E, bool vec_ok, F f) {
@@ -689,32 +852,44 @@ void with_vec(int E, bool vec_ok, F f) {
     else
         f(std::integral_constant<int, VPL>(), std::integral_constant<int, 1>());
 }
-template <int DT, typename F>
+template <int DT, int L = kRowLanes, typename F>
 void with_row(int E, bool vec_ok, F f) {
-    if (E <= 16) with_vec<DT, 1>(E, vec_ok, f);
-    else if (E <= 32) with_vec<DT, 2>(E, vec_ok, f);
-    else if (E <= 64) with_vec<DT, 4>(E, vec_ok, f);
-    else if (E <= 128) with_vec<DT, 8>(E, vec_ok, f);
-    else if (E <= 256) with_vec<DT, 16>(E, vec_ok, f);
-    else if (E <= 512) with_vec<DT, 32>(E, vec_ok, f);
-    else with_vec<DT, 64>(E, vec_ok, f);
+    if (E <= L) with_vec<DT, 1>(E, vec_ok, f);
+    else if (E <= 2 * L) with_vec<DT, 2>(E, vec_ok, f);
+    else if (E <= 4 * L) with_vec<DT, 4>(E, vec_ok, f);
+    else if (E <= 8 * L) with_vec<DT, 8>(E, vec_ok, f);
+    else if (E <= 16 * L) with_vec<DT, 16>(E, vec_ok, f);
+    else if constexpr (L == kRowLanes) {
+        if (E <= 512) with_vec<DT, 32>(E, vec_ok, f);
+        else with_vec<DT, 64>(E, vec_ok, f);
+    }
 }
 
 unsigned row_blocks(int T) { return (unsigned)(((int64_t)T + kRowsPerBlock - 1) / kRowsPerBlock); }
 
-template <int DT>
+template <int DT, int L>
 void launch_gate(const moe_gate_shape_t* s, const moe_gate_options_t& o, const void* logits, const float* bias,
                  const uint8_t* mask, int64_t* idx, float* w, hipStream_t stream) {
     typedef typename Elem<DT>::type T;
-    with_row<DT>(s->E, aligned(logits, 16), [&](auto vpl, auto vec) {
+    const dim3 grid((unsigned)(((int64_t)s->T * L + kThreads - 1) / kThreads));
+    with_row<DT, L>(s->E, aligned(logits, 16), [&](auto vpl, auto vec) {
         constexpr int VPL = decltype(vpl)::value, VEC = decltype(vec)::value;
         if (bias)
-            hipLaunchKernelGGL((k_gate<DT, VPL, VEC, true>), dim3(row_blocks(s->T)), dim3(kThreads), 0, stream,
-                               (const T*)logits, bias, mask, s->T, s->E, s->K, o.score, o.renormalise, o.scale, idx, w);
+            hipLaunchKernelGGL((k_gate<DT, VPL, VEC, true, L>), grid, dim3(kThreads), 0, stream, (const T*)logits, bias,
+                               mask, s->T, s->E, s->K, o.score, o.renormalise, o.scale, idx, w);
         else
-            hipLaunchKernelGGL((k_gate<DT, VPL, VEC, false>), dim3(row_blocks(s->T)), dim3(kThreads), 0, stream,
-                               (const T*)logits, bias, mask, s->T, s->E, s->K, o.score, o.renormalise, o.scale, idx, w);
+            hipLaunchKernelGGL((k_gate<DT, VPL, VEC, false, L>), grid, dim3(kThreads), 0, stream, (const T*)logits, bias,
+                               mask, s->T, s->E, s->K, o.score, o.renormalise, o.scale, idx, w);
     });
+}
+
+// A wave per row while that leaves at most one wave on a SIMD, four rows a
+// wave above.
+template <int DT>
+void launch_gate(const moe_gate_shape_t* s, const moe_gate_options_t& o, const void* logits, const float* bias,
+                 const uint8_t* mask, int64_t* idx, float* w, hipStream_t stream) {
+    if (s->T <= 4 * device_cus()) launch_gate<DT, 64>(s, o, logits, bias, mask, idx, w, stream);
+    else launch_gate<DT, kRowLanes>(s, o, logits, bias, mask, idx, w, stream);
 }
 
 template <int DT>
@@ -840,7 +1015,8 @@ int moe_balance_loss(const moe_gate_shape_t* s, const moe_gate_options_t* opt, c
         launch_balance_part<MOE_DTYPE_BF16>(s, o.score, logits, token_mask, topk_idx, seq_offsets, S, ws, blocks, stream);
     const int64_t items = (int64_t)S * ((s->E + kFinalExperts - 1) / kFinalExperts);
     int lanes = 1;
-    while (lanes < kWave && (int64_t)lanes * S < chunks) lanes <<= 1;
+    // lanes that count a sequence's live tokens: as many as it has chunks, all sequences at once if possible
+    while (lanes < kWave && (int64_t)lanes * S < chunks && (int64_t)2 * lanes * S <= kFinalThreads / 2) lanes <<= 1;
     hipLaunchKernelGGL(k_balance_final, dim3((unsigned)(items < kFinalBlocks ? items : kFinalBlocks)),
                        dim3(kFinalThreads), 0, stream, s->T, s->E, seq_offsets, S, coef, loss, counts, slope, ws, lanes);
     return launch_status();
