@@ -137,7 +137,9 @@ __device__ __forceinline__ void store_row(typename Elem<DT>::type* row, int E, i
     }
 }
 
-__device__ __forceinline__ float sigmoid(float l) { return 1.f / (1.f + expf(-l)); }
+// v_rcp_f32 is good to a step; with expf's two and the sum's half the result
+// errs by less than 10 half-steps.
+__device__ __forceinline__ float sigmoid(float l) { return __builtin_amdgcn_rcpf(1.f + expf(-l)); }
 __device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-(double)l)); }
 
 // An unsigned key in the order of v: -0 = +0, NaN above all, never 0 (0 marks
@@ -568,7 +570,8 @@ __global__ __launch_bounds__(kThreads) void k_gate_backward(
 }
 
 // ---- balance loss -----------------------------------------------------------------
-// Two launches.  k_balance_part: a block per chunk of kChunk tokens adds up,
+// A small batch of one sequence: k_balance_one.  Else two launches.
+// k_balance_part: a block per chunk of kChunk tokens adds up,
 // for each sequence q that the chunk b meets, the probabilities and the slot
 // counts of every expert into row b + q of the partial tables.  Going through
 // the pairs (b, q) in token order each step raises b or q, so the rows differ,
@@ -588,6 +591,104 @@ struct BalanceWs {
     int32_t* part_c;    // [chunks + S][E]
 };
 
+// Logits -> scores normalised over the row; a row of -inf only -> zeros.
+template <int VPL>
+__device__ __forceinline__ void probabilities(float (&v)[VPL], bool soft) {
+    float top = 0.f, total = 0.f;
+    if (soft) {
+        top = v[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) top = fmaxf(top, v[i]);
+        top = row_max(top);
+        top = top == -INFINITY ? 0.f : top;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        v[i] = soft ? expf(v[i] - top) : sigmoid(v[i]);
+        total += v[i];
+    }
+    total = row_sum(total);
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] *= inv;
+}
+// The sum over the four rows of a wave, in every lane.
+__device__ __forceinline__ float sum_of_rows(float v) {
+    return __uint_as_float(across_rows(__float_as_uint(v), [](uint32_t x, uint32_t y) {
+        return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+    }));
+}
+
+// One sequence of a small batch: everything in one workgroup and one launch
+// (each of the two launches below is 5 us of latency for any batch).
+constexpr int kOneThreads = 1024;
+template <int DT, int VPL, int VEC>
+__global__ __launch_bounds__(kOneThreads) void k_balance_one(
+    const typename Elem<DT>::type* __restrict__ logits, const uint8_t* __restrict__ mask,
+    const int64_t* __restrict__ topk_idx, int T, int E, int K, int score, const int32_t* __restrict__ seq_offsets,
+    float coef, float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ slope) {
+    constexpr int kWaves = kOneThreads / kWave, kGroups = kOneThreads / kRowLanes;
+    extern __shared__ float lds_one[];  // [kWaves][E] probability sums, then [E] counts
+    __shared__ int lds_n[2];
+    __shared__ double lds_loss[kWaves];
+    int* lds_c = reinterpret_cast<int*>(lds_one + kWaves * E);
+    const int tid = threadIdx.x, j = tid & (kRowLanes - 1), wave = tid / kWave;
+    for (int e = tid; e < E; e += kOneThreads) lds_c[e] = 0;
+    if (tid < 2) lds_n[tid] = 0;
+    int lo, hi;
+    sequence_range(seq_offsets, 0, T, lo, hi);
+    __syncthreads();
+    int found = 0, tokens = 0;
+    for (int i = tid; i < (hi - lo) * K; i += kOneThreads) {
+        const int64_t e = topk_idx[(int64_t)lo * K + i];
+        if (e >= 0 && e < E && !(mask && !mask[lo + i / K])) {
+            atomicAdd(&lds_c[e], 1);
+            ++found;
+        }
+    }
+    float acc[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+    for (int t = lo + tid / kRowLanes; t < hi; t += kGroups) {
+        if (mask && !mask[t]) continue;
+        ++tokens;
+        float v[VPL];
+        load_row<DT, VPL, VEC>(logits + (int64_t)t * E, E, j, v);
+        probabilities<VPL>(v, score == MOE_SCORE_SOFTMAX);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) acc[i] += v[i];
+    }
+    if (tokens && j == 0) atomicAdd(&lds_n[0], tokens);
+    if (found) atomicAdd(&lds_n[1], found);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const float s = sum_of_rows(acc[i]);
+        const int e = expert_of<VEC>(i, j);
+        if ((tid & (kWave - 1)) < kRowLanes && e < E) lds_one[wave * E + e] = s;
+    }
+    __syncthreads();
+    const int n = lds_n[0], m = lds_n[1];
+    double part = 0.0;
+    for (int e = tid; e < E; e += kOneThreads) {
+        double p = 0.0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) p += (double)lds_one[w * E + e];
+        const int c = lds_c[e];
+        const double f = n > 0 && m > 0 ? (double)coef * E * c / ((double)m * n) : 0.0;
+        counts[e] = c;
+        slope[e] = (float)f;
+        part += f * p;
+    }
+    for (int x = 1; x < kWave; x <<= 1) part += __shfl_xor(part, x);
+    if (tid % kWave == 0) lds_loss[wave] = part;
+    __syncthreads();
+    if (tid == 0) {
+        double all = 0.0;
+        for (int w = 0; w < kWaves; ++w) all += lds_loss[w];
+        *loss = (float)all;
+    }
+}
+
 template <int DT, int VPL, int VEC>
 __global__ __launch_bounds__(kThreads) void k_balance_part(
     const typename Elem<DT>::type* __restrict__ logits, const uint8_t* __restrict__ mask,
@@ -605,6 +706,8 @@ __global__ __launch_bounds__(kThreads) void k_balance_part(
     if (t0 >= T) return;  // T == 0
     const bool soft = score == MOE_SCORE_SOFTMAX;
 
+    for (int e = tid; e < E; e += kThreads) lds_c[e] = 0;
+    if (tid < 2) lds_n[tid] = 0;
     // everything of the chunk's tokens, before it is known whose they are: a
     // lane group's rows as probabilities (0 for padding), a thread's slots
     float p[kRows][VPL];
@@ -642,25 +745,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_part(
         q = sequence_of(seq_offsets, S, t0, j);
     }
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        float top = 0.f, total = 0.f;
-        if (soft) {
-            top = p[r][0];
-#pragma unroll
-            for (int i = 1; i < VPL; ++i) top = fmaxf(top, p[r][i]);
-            top = row_max(top);
-            top = top == -INFINITY ? 0.f : top;
-        }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            p[r][i] = soft ? expf(p[r][i] - top) : sigmoid(p[r][i]);
-            total += p[r][i];
-        }
-        total = row_sum(total);
-        const float inv = total == 0.f ? 0.f : 1.f / total;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) p[r][i] *= inv;
-    }
+    for (int r = 0; r < kRows; ++r) probabilities<VPL>(p[r], soft);
 
     for (; q < S; ++q) {
         int lo, hi;
@@ -669,9 +754,6 @@ __global__ __launch_bounds__(kThreads) void k_balance_part(
         lo = lo < t0 ? t0 : lo;
         hi = hi < t1 ? hi : t1;
         if (lo >= hi) continue;
-        __syncthreads();
-        for (int e = tid; e < E; e += kThreads) lds_c[e] = 0;
-        if (tid < 2) lds_n[tid] = 0;
         __syncthreads();
         int found = 0;
 #pragma unroll
@@ -697,8 +779,7 @@ __global__ __launch_bounds__(kThreads) void k_balance_part(
             acc[i] = 0.f;
 #pragma unroll
             for (int r = 0; r < kRows; ++r) acc[i] += in[r] ? p[r][i] : 0.f;
-            acc[i] += __shfl_xor(acc[i], 16);
-            acc[i] += __shfl_xor(acc[i], 32);
+            acc[i] = sum_of_rows(acc[i]);
             const int e = expert_of<VEC>(i, j);
             if ((tid & (kWave - 1)) < kRowLanes && e < E) lds_sum[wave * E + e] = acc[i];
         }
@@ -707,8 +788,12 @@ __global__ __launch_bounds__(kThreads) void k_balance_part(
         for (int e = tid; e < E; e += kThreads) {
             ws.part_p[at + e] = (lds_sum[e] + lds_sum[E + e]) + (lds_sum[2 * E + e] + lds_sum[3 * E + e]);
             ws.part_c[at + e] = lds_c[e];
+            lds_c[e] = 0;  // for the next sequence
         }
-        if (tid == 0) ws.pair_n[b + q] = make_int2(lds_n[0], lds_n[1]);
+        if (tid == 0) {
+            ws.pair_n[b + q] = make_int2(lds_n[0], lds_n[1]);
+            lds_n[0] = lds_n[1] = 0;
+        }
     }
 }
 
@@ -719,7 +804,7 @@ __global__ __launch_bounds__(kFinalThreads) void k_balance_final(int T, int E, c
                                                                  int lanes_per_seq) {
     // The first half of the threads adds up work items; the second finds the
     // number of sequences with a live token meanwhile.
-    constexpr int kHalf = kFinalThreads / 2, kSlices = kHalf / kFinalExperts;
+    constexpr int kHalf = kFinalThreads / 2, kSlices = kHalf / kFinalExperts, kBatch = 16;
     __shared__ double lds_p[kSlices][kFinalExperts];
     __shared__ int lds_c[kSlices][kFinalExperts];
     __shared__ int lds_live[kHalf / kWave];
@@ -740,11 +825,11 @@ __global__ __launch_bounds__(kFinalThreads) void k_balance_final(int T, int E, c
             double p = 0.0;
             int c = 0;
             if (e < E)
-                for (int b = b0 + sl; b <= b1; b += 8 * kSlices) {  // eight rows' loads in flight
-                    float pv[8];
-                    int cv[8];
+                for (int b = b0 + sl; b <= b1; b += kBatch * kSlices) {  // the loads of kBatch rows in flight
+                    float pv[kBatch];
+                    int cv[kBatch];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
+                    for (int u = 0; u < kBatch; ++u) {
                         const bool in = b + u * kSlices <= b1;
                         const int64_t at = (int64_t)(in ? b + u * kSlices + q : b + q) * E + e;
                         pv[u] = ws.part_p[at];
@@ -752,7 +837,7 @@ __global__ __launch_bounds__(kFinalThreads) void k_balance_final(int T, int E, c
                         if (!in) pv[u] = 0.f, cv[u] = 0;
                     }
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
+                    for (int u = 0; u < kBatch; ++u) {
                         p += (double)pv[u];
                         c += cv[u];
                     }
@@ -819,10 +904,13 @@ __global__ __launch_bounds__(kFinalThreads) void k_balance_final(int T, int E, c
         }
         __syncthreads();
     }
+    // The block's loss goes out by an agent-scope store, which passes the
+    // caches that other XCDs do not see, and has arrived before the count goes
+    // up; a release of everything written would flush the whole L2 instead.
     if (tid == 0) {
         __hip_atomic_store(&ws.loss_part[blockIdx.x], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const uint32_t before =
-            __hip_atomic_fetch_add(ws.arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const uint32_t before = __hip_atomic_fetch_add(ws.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         lds_last = before == gridDim.x - 1;
     }
     __syncthreads();
@@ -918,6 +1006,27 @@ void launch_balance_part(const moe_gate_shape_t* s, int score, const void* logit
     });
 }
 
+// Up to 512 tokens and 16384 logits.  Measured, one launch and two: 1 x 128 4.4
+// and 10 us, 64 x 256 7.4 and 14, 128 x 128 8.9 and 12, 509 x 32 11 and 11 (and
+// the host's 3 us for a launch), 2048 x 8 20 and 11.
+constexpr int64_t kOneLogits = 16384;
+bool fits_one(const moe_gate_shape_t* s, int32_t S) {
+    return S == 1 && s->E <= 512 && s->T <= 512 && (int64_t)s->T * s->E <= kOneLogits;
+}
+template <int DT>
+void launch_balance_one(const moe_gate_shape_t* s, int score, const void* logits, const uint8_t* mask,
+                        const int64_t* idx, const int32_t* seq_offsets, float coef, float* loss, int32_t* counts,
+                        float* slope, hipStream_t stream) {
+    typedef typename Elem<DT>::type T;
+    with_row<DT>(s->E, aligned(logits, 16), [&](auto vpl, auto vec) {
+        constexpr int VPL = decltype(vpl)::value, VEC = decltype(vec)::value;
+        if constexpr (VPL <= 32)
+            hipLaunchKernelGGL((k_balance_one<DT, VPL, VEC>), dim3(1), dim3(kOneThreads),
+                               sizeof(float) * (kOneThreads / kWave + 1) * s->E, stream, (const T*)logits, mask, idx,
+                               s->T, s->E, s->K, score, seq_offsets, coef, loss, counts, slope);
+    });
+}
+
 bool seq_ok(const moe_gate_shape_t* s, int32_t S) {
     return gate_shape_ok(s) && S >= 1 && S <= 65536 && (int64_t)S * s->E < (int64_t(1) << 31);
 }
@@ -1005,6 +1114,15 @@ int moe_balance_loss(const moe_gate_shape_t* s, const moe_gate_options_t* opt, c
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < balance_layout(s, S, nullptr, nullptr))
         return MOE_ERR_WORKSPACE;
     if (!device_ok()) return MOE_ERR_DEVICE;
+    if (fits_one(s, S)) {
+        if (o.dtype == MOE_DTYPE_F32)
+            launch_balance_one<MOE_DTYPE_F32>(s, o.score, logits, token_mask, topk_idx, seq_offsets, coef, loss, counts,
+                                              slope, stream);
+        else
+            launch_balance_one<MOE_DTYPE_BF16>(s, o.score, logits, token_mask, topk_idx, seq_offsets, coef, loss, counts,
+                                               slope, stream);
+        return launch_status();
+    }
     BalanceWs ws;
     balance_layout(s, S, static_cast<uint8_t*>(workspace), &ws);
     const int64_t chunks = ((int64_t)s->T + kChunk - 1) / kChunk;
