@@ -53,6 +53,12 @@ __device__ __forceinline__ void dma_x4(uint32_t lds, const void* sbase, uint32_t
                  "v"(voff), "s"(uniform_ptr(sbase))
                  : "memory");
 }
+__device__ __forceinline__ void dma_x4_nt(uint32_t lds, const void* sbase, uint32_t voff) {  // non-temporal
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(
+                     __builtin_amdgcn_readfirstlane(lds)),
+                 "v"(voff), "s"(uniform_ptr(sbase))
+                 : "memory");
+}
 __device__ __forceinline__ void dma_x1(uint32_t lds, const void* sbase, uint32_t voff) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(
                      __builtin_amdgcn_readfirstlane(lds)),
@@ -98,8 +104,9 @@ __device__ __forceinline__ void group_rows(const BlockArgs& g, int e, int& lo, i
     n = clamp_int(g.offsets[e + 1], lo, (int)g.R) - lo;
 }
 
-template <int MODE_, int WQ_, int WP_, int J_, int TT_, int STAGES_, int GROUP_, int PER_CU_>
+template <int MODE_, int WQ_, int WP_, int J_, int TT_, int STAGES_, int GROUP_, int PER_CU_, bool STREAM_Q_ = false>
 struct Cfg {
+    static constexpr bool STREAM_Q = STREAM_Q_;  // Q goes by the caches
     static constexpr int MODE = MODE_, WQ = WQ_, WP = WP_, J = J_, TT = TT_, STAGES = STAGES_, GROUP = GROUP_,
                          PER_CU = PER_CU_;
     static constexpr int BQ = 32 * J * WQ, BP = 32 * TT * WP, WAVES = WQ * WP, THREADS = 64 * WAVES;
@@ -292,7 +299,9 @@ struct Loader {
         dma_x4(lds + w.wave * 1024 + i * C::THREADS * 16, p, po[i]);
     }
     __device__ __forceinline__ void load_q(const Place<C>& w, uint32_t lds, int i) const {
-        dma_x4(lds + C::QOFF + w.wave * 1024 + i * C::THREADS * 16, q, qo[i]);
+        const uint32_t at = lds + C::QOFF + w.wave * 1024 + i * C::THREADS * 16;
+        if (C::STREAM_Q) dma_x4_nt(at, q, qo[i]);
+        else dma_x4(at, q, qo[i]);
     }
     __device__ __forceinline__ void load_scales(const Place<C>& w, uint32_t lds) const {
         const bool rw = w.wave < C::BP / 64;
@@ -410,17 +419,18 @@ struct Frags {
             n = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(q[j % QSETS][0], p[i][0], n, 0, 0, 0, 0, 0, 0);
             asm volatile("" : "+v"(n));
             __builtin_amdgcn_sched_barrier(0);
-            // half of the pending adds behind each MFMA: a 64-cycle MFMA leaves
-            // a wave about 15 issue slots
+            // the pending adds behind both MFMAs: a 64-cycle MFMA leaves a wave
+            // about 15 issue slots, and the loads go out behind the second (10 + 6
+            // measured 1.5 % faster than 8 + 8, 0.7 % than 12 + 4)
 #pragma unroll
-            for (int r = 0; r < 8; ++r) acc[v / C::TT][v % C::TT][r] += part[(u + 1) & 1][r] * late;
+            for (int r = 0; r < 10; ++r) acc[v / C::TT][v % C::TT][r] += part[(u + 1) & 1][r] * late;
             asm volatile("" : "+v"(acc[v / C::TT][v % C::TT]));
             __builtin_amdgcn_sched_barrier(0);
             n = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(q[j % QSETS][1], p[i][1], n, 0, 0, 0, 0, 0, 0);
             asm volatile("" : "+v"(n));
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int r = 8; r < 16; ++r) acc[v / C::TT][v % C::TT][r] += part[(u + 1) & 1][r] * late;
+            for (int r = 10; r < 16; ++r) acc[v / C::TT][v % C::TT][r] += part[(u + 1) & 1][r] * late;
             asm volatile("" : "+v"(acc[v / C::TT][v % C::TT]));
             __builtin_amdgcn_sched_barrier(0);
             part[u & 1] = n;
@@ -637,17 +647,17 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block(
             ld.advance(g, w, rec, steps, ntiles);
             wait_and_meet<2>();
             __builtin_amdgcn_s_setprio(1);
-            f.multiply(acc, 2, 0);
             ld.load_p(w, here, 0);
+            f.multiply(acc, 2, 0);
             ld.load_p(w, here, 1);
-            f.multiply(acc, 2, 1);
             ld.load_p(w, here, 2);
+            f.multiply(acc, 2, 1);
             ld.load_p(w, here, 3);
-            f.multiply(acc, 3, 0);
             ld.load_q(w, here, 0);
+            f.multiply(acc, 3, 0);
             ld.load_q(w, here, 2);
-            f.multiply(acc, 3, 1);
             ld.load_scales(w, here);
+            f.multiply(acc, 3, 1);
             __builtin_amdgcn_s_setprio(0);
             meet();
             stage ^= (uint32_t)C::STAGE;
@@ -856,7 +866,8 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_block_thin(BlockArgs g) {
 
 // ---- host -----------------------------------------------------------------------
 typedef Cfg<kProduct, 2, 4, 4, 2, 2, 4, 1> BigProduct;  // 256 x 256, 8 waves of 64 x 128
-typedef Cfg<kProduct, 4, 1, 1, 2, 3, 1, 2> SmallProduct;  // 64 rows x 128, 4 waves of 64 x 32
+template <bool STREAM_Q>
+using SmallProduct = Cfg<kProduct, 4, 1, 1, 2, 3, 1, 2, STREAM_Q>;  // 64 rows x 128, 4 waves of 64 x 32
 typedef Cfg<kWgrad, 2, 4, 4, 2, 2, 4, 1> BigWgrad;
 
 template <class C>
@@ -911,10 +922,18 @@ void launch_product(const BlockArgs& g, hipStream_t stream) {
             return;
         }
     }
-    if (t_small < t_large)
-        launch<SmallProduct>(g, g.R / SmallProduct::BP + used, g.N, stream);
-    else
+    if (t_small < t_large) {
+        // Weights past one and a half times the 256 MB Infinity Cache, each read
+        // by one tile row, are streamed by it (32 groups of 32 rows, N 4096, K
+        // 7168, 940 MB: 165 us without the hint, 152 with it; 64 x 2048 x 2048,
+        // 268 MB: 44 and 48).
+        if ((int64_t)g.E * g.N * g.K > (int64_t(384) << 20) && per <= 64)
+            launch<SmallProduct<true>>(g, g.R / SmallProduct<true>::BP + used, g.N, stream);
+        else
+            launch<SmallProduct<false>>(g, g.R / SmallProduct<false>::BP + used, g.N, stream);
+    } else {
         launch<BigProduct>(g, g.R / BigProduct::BP + used, g.N, stream);
+    }
 }
 
 // An upper bound of the tiles of `p` rows in up to 1024 groups: the kernels count them in 32 bits.
