@@ -115,7 +115,8 @@ struct Cfg {
     static constexpr int LOADS = PP + QP + 1;                           // per wave and step
     static constexpr int QOFF = BP * kBK, SOFF = (BP + BQ) * kBK;
     static constexpr int TABLE_PRE = kMaxGroups + 4, TABLE_REC = THREADS * (MODE == kProduct ? 4 : 5);
-    static constexpr int TABLE = TABLE_PRE > TABLE_REC ? TABLE_PRE : TABLE_REC;
+    static constexpr int TABLE_FIRST = TABLE_PRE + (MODE == kWgrad ? kMaxGroups : 0);
+    static constexpr int TABLE = TABLE_FIRST > TABLE_REC ? TABLE_FIRST : TABLE_REC;
     static constexpr int STAGE = SOFF + (MODE == kProduct ? BP * 4 + 256 : WAVES * 256);
     static_assert(MODE == kProduct ? BP / 64 < WAVES : BP / 64 + BQ / 64 == WAVES, "a wave for every 64 scales");
     static_assert(ROWS % 16 == 0, "a thread's chunk does not depend on the pass");
@@ -488,16 +489,49 @@ __device__ __forceinline__ int plan_tiles(const BlockArgs& g, const Place<C>& w,
     // XCD x (workgroups go round-robin over the 8) takes the x-th contiguous
     // eighth of the tile order, so that its L2 sees neighbouring tiles; its
     // workgroups take them in turn, at most THREADS each (the launch sees to it).
+    // wgrad, whose groups differ in K steps: an eighth of every group's tiles
+    // instead, the largest groups first and the turn reversed every other time,
+    // so that XCDs and workgroups get the same work (32 groups of 1024 rows on
+    // average, sizes as rank^-0.6, N 1536, K 2048: 202 us in contiguous eighths, 161 so).
     const Order<C> o(g, pre);
-    const uint32_t xcd = blockIdx.x & 7, step = gridDim.x / 8;
-    const uint32_t end = (uint32_t)((uint64_t)o.total * (xcd + 1) / 8);
-    const uint32_t idx = (uint32_t)((uint64_t)o.total * xcd / 8) + (blockIdx.x >> 3);
-    if (idx >= end) return 0;
-    const int ntiles = __builtin_amdgcn_readfirstlane((int)((end - idx + step - 1) / step));
+    const uint32_t xcd = blockIdx.x & 7, turn = blockIdx.x >> 3, step = gridDim.x / 8;
+    const uint32_t each = (uint32_t)(o.np * o.nq), lo = each * xcd / 8, share = each * (xcd + 1) / 8 - lo;
+    const bool spread = C::MODE == kWgrad && (each % 8 == 0 || each >= 32);
+    const uint32_t begin = spread ? 0u : (uint32_t)((uint64_t)o.total * xcd / 8);
+    const uint32_t count = spread ? (uint32_t)g.E * share : (uint32_t)((uint64_t)o.total * (xcd + 1) / 8) - begin;
+    const auto place = [&](uint32_t k) { return k * step + (spread && (k & 1) ? step - 1 - turn : turn); };
+    const uint32_t whole = count / step;
+    const int ntiles = __builtin_amdgcn_readfirstlane((int)(whole + (place(whole) < count ? 1 : 0)));
+    if (ntiles == 0) return 0;
+    int* order = table + C::TABLE_PRE;  // wgrad: the groups by falling K steps
+    if (spread) {
+        for (int e = w.tid; e < g.E; e += C::THREADS) {
+            int rank = e;
+            if (g.E <= 256) {
+                const int mine = pre[e + 1] - pre[e];
+                rank = 0;
+                for (int i = 0; i < g.E; ++i) {
+                    const int other = pre[i + 1] - pre[i];
+                    rank += other > mine || (other == mine && i < e);
+                }
+            }
+            order[rank] = e;
+        }
+        __syncthreads();
+    }
     TileRec t = {0, 0, 0, 0};
     int nk = 0;
     if (w.tid < ntiles) {
-        t = o.at(g, pre, idx + (uint32_t)w.tid * step);
+        const uint32_t i = begin + place((uint32_t)w.tid);
+        if (spread) {
+            const uint32_t c = lo + i % share;
+            t.z = order[i / share];
+            t.x = (int)(c % (uint32_t)o.np) * C::BP;
+            t.w = (int)(c / (uint32_t)o.np);
+            t.y = clamp_int(pre[t.z], 0, (int)(g.ld / kBK));
+        } else {
+            t = o.at(g, pre, i);
+        }
         if (C::MODE == kWgrad) nk = clamp_int(pre[t.z + 1], t.y, (int)(g.ld / kBK)) - t.y;
     }
     __syncthreads();
@@ -876,7 +910,7 @@ void launch(const BlockArgs& g, int64_t p_tiles, int q, hipStream_t stream) {
     const int64_t fill = (int64_t)(device_cus() / 8 * 8) * C::PER_CU;
     int64_t grid = most < fill ? (most + 7) / 8 * 8 : fill;
     // at most THREADS tiles a workgroup (those beyond the resident ones wait their turn)
-    const int64_t least = ((most + 7) / 8 + C::THREADS - 1) / C::THREADS * 8;
+    const int64_t least = ((most + 7) / 8 + g.E + C::THREADS - 1) / C::THREADS * 8;
     if (grid < least) grid = least;
     if constexpr (C::WAVES == 8)
         hipLaunchKernelGGL(k_block<C>, dim3((unsigned)grid), dim3(C::THREADS), 0, stream, g);
