@@ -356,15 +356,23 @@ private:
     }
 };
 
-// The sum side of one wave: operand fragments, scales and, for the product,
-// two partial tiles, so that one tile's scaled adds run while the next tile's
-// MFMAs do.
+// The sum side of one wave.  Pending (product): two partial tiles, so that one
+// tile's scaled adds run while the next tile's MFMAs do.
+struct Pending {
+    v16f part[2];
+    float late;  // the scale of the tile that is pending
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) part[1][r] = 0.f;
+        late = 0.f;
+    }
+};
+// Operand fragments and scales of a step.
 template <class C>
 struct Frags {
     static constexpr int QSETS = C::J < 2 ? 1 : 2;
     v8i p[C::TT][2], q[QSETS][2];  // q: tile j in set j % QSETS
-    v16f part[2];                  // product
-    float sc[C::TT], late;         // product: the step's scales; that of the pending partial tile
+    float sc[C::TT];               // product
     int sp[C::TT], sq[C::J];       // wgrad
 
     // Chunks 2 i + h, i = 0..3, of a row lie at its chunk h ^ key with i's bits
@@ -401,17 +409,10 @@ struct Frags {
             for (int j = 0; j < C::J; ++j) sq[j] = k.q(s, q_row<C::J>((w.wq * C::J + j) * 32 + (w.lane & 31)));
         }
     }
-    __device__ __forceinline__ void clear() {
-        if (C::MODE == kProduct) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) part[1][r] = 0.f;
-            late = 0.f;
-        }
-    }
     // The empty asm statements keep sums and MFMAs where they are written: the
     // compiler would sink them behind the next branch, with all their operands
     // alive until there.
-    __device__ __forceinline__ void multiply(v16f (&acc)[C::J][C::TT], int j, int i) {
+    __device__ __forceinline__ void multiply(v16f (&acc)[C::J][C::TT], Pending& d, int j, int i) const {
         constexpr int U = C::J * C::TT;
         static_assert(U % 2 == 0, "partial tiles alternate");
         if (C::MODE == kProduct) {
@@ -424,18 +425,18 @@ struct Frags {
             // about 15 issue slots, and the loads go out behind the second (10 + 6
             // measured 1.5 % faster than 8 + 8, 0.7 % than 12 + 4)
 #pragma unroll
-            for (int r = 0; r < 10; ++r) acc[v / C::TT][v % C::TT][r] += part[(u + 1) & 1][r] * late;
+            for (int r = 0; r < 10; ++r) acc[v / C::TT][v % C::TT][r] += d.part[(u + 1) & 1][r] * d.late;
             asm volatile("" : "+v"(acc[v / C::TT][v % C::TT]));
             __builtin_amdgcn_sched_barrier(0);
             n = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(q[j % QSETS][1], p[i][1], n, 0, 0, 0, 0, 0, 0);
             asm volatile("" : "+v"(n));
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int r = 10; r < 16; ++r) acc[v / C::TT][v % C::TT][r] += part[(u + 1) & 1][r] * late;
+            for (int r = 10; r < 16; ++r) acc[v / C::TT][v % C::TT][r] += d.part[(u + 1) & 1][r] * d.late;
             asm volatile("" : "+v"(acc[v / C::TT][v % C::TT]));
             __builtin_amdgcn_sched_barrier(0);
-            part[u & 1] = n;
-            late = sc[i];
+            d.part[u & 1] = n;
+            d.late = sc[i];
         } else {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
@@ -444,13 +445,16 @@ struct Frags {
             asm volatile("" : "+v"(acc[j][i]));
         }
     }
-    __device__ __forceinline__ void finish(v16f (&acc)[C::J][C::TT]) {
-        if (C::MODE == kProduct) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[C::J - 1][C::TT - 1][r] += part[1][r] * late;
-        }
-    }
 };
+
+// The last tile's pending adds.
+template <class C>
+__device__ __forceinline__ void finish(v16f (&acc)[C::J][C::TT], const Pending& d) {
+    if (C::MODE == kProduct) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[C::J - 1][C::TT - 1][r] += d.part[1][r] * d.late;
+    }
+}
 
 // Fills `table` with the workgroup's tile records; their number, 0 if it has none.
 template <class C>
@@ -569,34 +573,35 @@ __device__ __forceinline__ void store(const BlockArgs& g, const Place<C>& w, con
                                                pack_bf16x2(acc[j + 1][i][4 * a + 2], acc[j + 1][i][4 * a + 3]));
                     if (q + 4 * j < t.cols) *reinterpret_cast<uint4*>(o + q + 4 * j) = v;
                 }
-            } else if (g.wide) {
+            } else {
 #pragma unroll
                 for (int j = 0; j < C::J; ++j) {
                     const uint2 v = make_uint2(pack_bf16x2(acc[j][i][4 * a], acc[j][i][4 * a + 1]),
                                                pack_bf16x2(acc[j][i][4 * a + 2], acc[j][i][4 * a + 3]));
-                    if (q + 4 * j < t.cols) *reinterpret_cast<uint2*>(o + q + 4 * j) = v;
+                    uint16_t* at = o + q + 4 * j;
+                    if (q + 4 * j + 3 < t.cols) {
+                        if (g.wide) *reinterpret_cast<uint2*>(at) = v;
+                        else __builtin_memcpy(at, &v, 8);  // on a 2-byte boundary: the hardware splits it
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 3; ++x)
+                            if (q + 4 * j + x < t.cols) at[x] = (uint16_t)((x < 2 ? v.x : v.y) >> (16 * (x & 1)));
+                    }
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < C::J; ++j)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (q + 4 * j + x < t.cols)
-                            o[q + 4 * j + x] = (uint16_t)pack_bf16x2(acc[j][i][4 * a + x], 0.f);
             }
         }
     }
 }
 
 template <class C>
-__device__ __forceinline__ void clear_sums(v16f (&acc)[C::J][C::TT], Frags<C>& f) {
+__device__ __forceinline__ void clear_sums(v16f (&acc)[C::J][C::TT], Pending& d) {
 #pragma unroll
     for (int j = 0; j < C::J; ++j)
 #pragma unroll
         for (int i = 0; i < C::TT; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.f;
-    f.clear();
+    if (C::MODE == kProduct) d.clear();
 }
 
 // Many rows a group.  Eight waves, two on each SIMD: waves 0-3 and waves 4-7
@@ -650,6 +655,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block(
     if (!first) meet();
 
     Frags<C> f;
+    Pending d;
     uint32_t stage = 0;  // LDS offset of the current step's stage
     for (int n = 0; n < ntiles; ++n) {
         Tile<C> t;
@@ -657,7 +663,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block(
         ScaleSkew<C> skew;
         skew.open(g, t);
         v16f acc[C::J][C::TT];
-        clear_sums(acc, f);
+        clear_sums<C>(acc, d);
 
         for (int k = 0; k < t.nk; ++k) {
             const uint32_t here = base + stage, there = base + (stage ^ (uint32_t)C::STAGE);
@@ -667,12 +673,12 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block(
             f.read_scales(w, lds + stage, skew, prow);
             wait_and_meet<7>();
             __builtin_amdgcn_s_setprio(1);
-            f.multiply(acc, 0, 0);
+            f.multiply(acc, d, 0, 0);
             ld.load_q(w, there, 1);
-            f.multiply(acc, 0, 1);
-            f.multiply(acc, 1, 0);
+            f.multiply(acc, d, 0, 1);
+            f.multiply(acc, d, 1, 0);
             ld.load_q(w, there, 3);
-            f.multiply(acc, 1, 1);
+            f.multiply(acc, d, 1, 1);
             __builtin_amdgcn_s_setprio(0);
             meet();
 
@@ -682,22 +688,22 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block(
             wait_and_meet<2>();
             __builtin_amdgcn_s_setprio(1);
             ld.load_p(w, here, 0);
-            f.multiply(acc, 2, 0);
+            f.multiply(acc, d, 2, 0);
             ld.load_p(w, here, 1);
             ld.load_p(w, here, 2);
-            f.multiply(acc, 2, 1);
+            f.multiply(acc, d, 2, 1);
             ld.load_p(w, here, 3);
             ld.load_q(w, here, 0);
-            f.multiply(acc, 3, 0);
+            f.multiply(acc, d, 3, 0);
             ld.load_q(w, here, 2);
             ld.load_scales(w, here);
-            f.multiply(acc, 3, 1);
+            f.multiply(acc, d, 3, 1);
             __builtin_amdgcn_s_setprio(0);
             meet();
             stage ^= (uint32_t)C::STAGE;
             skew.next(g);
         }
-        f.finish(acc);
+        finish<C>(acc, d);
         store(g, w, t, acc);
     }
     if (first) meet();
@@ -730,33 +736,44 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block_
     }
 
     const ScaleSkew<C> skew = {};
-    Frags<C> f;
+    Frags<C> even, odd;
+    Pending d;
     uint32_t stage = 0;  // LDS offset of the current step's stage
     wait_and_meet<C::LOADS*(C::STAGES - 1)>();
-    f.read_scales(w, lds, skew, prow);
-    f.read_p(lds, pr);
-    f.read_q(lds, qr, 0);
+    const auto read = [&](Frags<C>& f, uint32_t at) {
+        f.read_p(lds, pr + at);
+        f.read_q(lds, qr + at, 0);
+        f.read_scales(w, lds + at, skew, prow);
+    };
+    read(even, 0);
     for (int n = 0; n < ntiles; ++n) {
         Tile<C> t;
         t.read(g, rec, nullptr, n);
         v16f acc[C::J][C::TT];
-        clear_sums(acc, f);
-        for (int k = 0; k < t.nk; ++k) {
+        clear_sums<C>(acc, d);
+        // One step: this stage's fragments are in `now`, so the next stage's
+        // loads are waited for, the workgroup meets, this stage goes to the step
+        // STAGES ahead, and the next fragments are read under the MFMAs.
+        const auto step = [&](const Frags<C>& now, Frags<C>& then) {
             const uint32_t next = stage + C::STAGE == C::STAGES * C::STAGE ? 0u : stage + C::STAGE;
-            // the fragments of this stage are in registers: the next stage's
-            // loads are waited for, the workgroup meets, and this stage goes to
-            // the step STAGES ahead
             wait_and_meet<C::LOADS*(C::STAGES - 2)>();
+            read(then, next);
             ld.load_all(w, lds_addr(lds) + stage);
 #pragma unroll
-            for (int i = 0; i < C::TT; ++i) f.multiply(acc, 0, i);
-            f.read_p(lds, pr + next);
-            f.read_q(lds, qr + next, 0);
-            f.read_scales(w, lds + next, skew, prow);
+            for (int i = 0; i < C::TT; ++i) now.multiply(acc, d, 0, i);
             stage = next;
             ld.advance(g, w, rec, nullptr, ntiles);
+        };
+        int k = 0;
+        for (; k + 1 < t.nk; k += 2) {
+            step(even, odd);
+            step(odd, even);
         }
-        f.finish(acc);
+        if (k < t.nk) {
+            step(even, odd);
+            even = odd;
+        }
+        finish<C>(acc, d);
         store(g, w, t, acc);
     }
     wait_loads<0>();  // no load may write LDS once the workgroup is gone
