@@ -23,6 +23,8 @@
 // (r / 4) * 4J + 4j + r % 4 of them, so that a lane ends up with 4J adjacent
 // outputs of a row.
 // The k order inside a 64-wide MFMA is the same permutation for both operands.
+#include <algorithm>
+
 #include "../../include/moe_block8.h"
 #include "moe_device.hpp"
 #include "moe_host.hpp"
@@ -949,11 +951,13 @@ void launch_thin(const BlockArgs& g, hipStream_t stream) {
 // Which kernel a product runs.  Tiles are counted for evenly filled groups
 // (half a tile a group is lost on the last one).  Measured times of a K step:
 // 256 x 256 tiles 1.3 us for up to 256 of them (one per CU), 64 x 128 tiles
-// 0.54 us for up to 256 and then in proportion (1.1 us for 512, two per CU).
-//   one group, K 7168, N 4096: 1024 rows 66 us with small tiles, 76 with large;
-//   2048 rows 129 and 86.  K 2048, N 2048: 2048 rows 20 and 30, 4096 rows 34
-//   and 33.  32 groups, K 7168, N 4096: 64 rows each 175 and 226, 128 rows each
-//   324 and 228.
+// 0.54 us for up to 256 and then in proportion (1.1 us for 512, two per CU);
+// and the weights of all groups stream in at 6.0 TB/s at best with small tiles,
+// 4.4 with large ones.
+//   one group, K 7168, N 4096: 2048 rows 129 us with small tiles, 72 with large.
+//   K 2048, N 2048: 2048 rows 19 and 27, 4096 rows 31 and 30.  32 groups, K
+//   7168, N 4096: 48 rows each on average 162 and 206, 64 rows 241 and 210
+//   (every second group needs a second row of small tiles), 128 rows 353 and 223.
 // With at most 64 rows a group and few tiles, K is split instead: a round of
 // one 16-output workgroup per CU takes 0.20, 0.30 or 0.45 us for each K step
 // with 16, 32 or 64 rows.
@@ -961,8 +965,10 @@ void launch_product(const BlockArgs& g, hipStream_t stream) {
     const int64_t used = g.E < g.R ? g.E : g.R, per = (g.R + used - 1) / used, cus = device_cus();
     const int64_t small = ((g.R + used * 32) / 64 > used ? (g.R + used * 32) / 64 : used) * ((g.N + 127) / 128);
     const int64_t large = ((g.R + used * 128) / 256 > used ? (g.R + used * 128) / 256 : used) * ((g.N + 255) / 256);
-    const double t_small = 0.54 * (double)(small > cus ? small : cus) / (double)cus;
-    const double t_large = 1.3 * (double)((large + cus - 1) / cus);
+    const double weights = 1e-6 * 128.0 * (double)used * g.N;  // MB of a K step
+    const double reads = (double)small / (double)(used * ((g.N + 127) / 128));  // of a group's weights
+    const double t_small = std::max(0.54 * (double)(small > cus ? small : cus) / (double)cus, weights * reads / 6.0);
+    const double t_large = std::max(1.3 * (double)((large + cus - 1) / cus), weights / 4.4);
     if (per <= 64) {
         const int64_t thin = (g.offsets ? g.R / 64 + used : 1) * ((g.N + 15) / 16);
         const double step = per <= 16 ? 0.15 : per <= 32 ? 0.25 : 0.35;
