@@ -966,7 +966,11 @@ void launch_product(const BlockArgs& g, hipStream_t stream) {
     const int64_t small = ((g.R + used * 32) / 64 > used ? (g.R + used * 32) / 64 : used) * ((g.N + 127) / 128);
     const int64_t large = ((g.R + used * 128) / 256 > used ? (g.R + used * 128) / 256 : used) * ((g.N + 255) / 256);
     const double weights = 1e-6 * 128.0 * (double)used * g.N;  // MB of a K step
-    const double reads = (double)small / (double)(used * ((g.N + 127) / 128));  // of a group's weights
+    // how often a group's weights come from memory: once for each row of small
+    // tiles, unless all of them fit the Infinity Cache
+    const double reads = used * g.N * (int64_t)g.K <= (int64_t(256) << 20)
+                             ? 1.0
+                             : (double)small / (double)(used * ((g.N + 127) / 128));
     const double t_small = std::max(0.54 * (double)(small > cus ? small : cus) / (double)cus, weights * reads / 6.0);
     const double t_large = std::max(1.3 * (double)((large + cus - 1) / cus), weights / 4.4);
     if (per <= 64) {

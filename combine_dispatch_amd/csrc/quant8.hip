@@ -347,7 +347,7 @@ bool elem_aligned(const void* p, int dt) { return aligned(p, dt == MOE_DTYPE_F32
 // whole 8-value vectors on 16-byte boundaries in every row
 bool vectors(const void* p, int cols) { return aligned(p, 16) && cols % 8 == 0; }
 
-// Inputs and outputs that together pass one and a half times the 256 MB
+// Inputs and outputs that together reach one and a half times the 256 MB
 // Infinity Cache go by it: little of them would be there for the next reader,
 // and a stream without the hint stays below 6.3 TB/s.  Measured without and
 // with it: rows 131072 x 2048 (805 MB) 154 and 135 us, weights 32 x 1536 x 2048
@@ -360,7 +360,7 @@ template <typename F>
 void with_input(int dt, bool vec, int64_t bytes, F f) {
     using std::integral_constant;
     const auto with = [&](auto d) {
-        if (vec && bytes > kCacheBytes) f(d, std::true_type(), std::true_type());
+        if (vec && bytes >= kCacheBytes) f(d, std::true_type(), std::true_type());
         else if (vec) f(d, std::true_type(), std::false_type());
         else f(d, std::false_type(), std::false_type());
     };
