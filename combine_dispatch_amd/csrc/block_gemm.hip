@@ -80,8 +80,6 @@ __device__ __forceinline__ void wait_and_meet() {
 }
 __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
 
-__device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
-
 struct BlockArgs {
     const uint8_t* p;
     const uint8_t* q;
@@ -95,15 +93,19 @@ struct BlockArgs {
     int wide;    // rows of out start on 16-byte boundaries
 };
 
-// Rows [lo, lo + n) of group e, inside 0..R whatever the offsets hold.
-__device__ __forceinline__ void group_rows(const BlockArgs& g, int e, int& lo, int& n) {
+// Rows [lo, lo + n) of group e.  False if its bounds are out of order or out
+// of 0..R: a kernel that finds such a group does nothing at all, so sums over
+// the groups never pass R and every index stays inside its array.
+__device__ __forceinline__ bool group_rows(const BlockArgs& g, int e, int& lo, int& n) {
     if (!g.offsets) {
         lo = 0;
         n = (int)g.R;
-        return;
+        return true;
     }
-    lo = clamp_int(g.offsets[e], 0, (int)g.R);
-    n = clamp_int(g.offsets[e + 1], lo, (int)g.R) - lo;
+    lo = g.offsets[e];
+    const int hi = g.offsets[e + 1];
+    n = hi - lo;
+    return lo >= 0 && lo <= hi && hi <= (int)g.R;
 }
 
 template <int MODE_, int WQ_, int WP_, int J_, int TT_, int STAGES_, int GROUP_, int PER_CU_, bool STREAM_Q_ = false>
@@ -176,7 +178,7 @@ struct Order {
         } else {
             t.z = m / np;
             t.x = m % np * C::BP;
-            t.y = clamp_int(pre[t.z], 0, (int)(g.ld / kBK));
+            t.y = pre[t.z];
         }
         return t;
     }
@@ -466,14 +468,16 @@ __device__ __forceinline__ int plan_tiles(const BlockArgs& g, const Place<C>& w,
         constexpr int kPer = kMaxGroups / C::THREADS;
         constexpr int kUnit = C::MODE == kProduct ? C::BP : kBK;
         int n[kPer], sum = 0;
+        bool sound = true;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = w.tid * kPer + i;
             int lo = 0, rows = 0;
-            if (e < g.E) group_rows(g, e, lo, rows);
+            if (e < g.E) sound &= group_rows(g, e, lo, rows);
             n[i] = (rows + kUnit - 1) / kUnit;
             sum += n[i];
         }
+        if (!__syncthreads_and(sound)) return 0;
         int before = sum;
         for (int d = 1; d < kWave; d <<= 1) {
             const int up = __shfl_up(before, d);
@@ -534,11 +538,11 @@ __device__ __forceinline__ int plan_tiles(const BlockArgs& g, const Place<C>& w,
             t.z = order[i / share];
             t.x = (int)(c % (uint32_t)o.np) * C::BP;
             t.w = (int)(c / (uint32_t)o.np);
-            t.y = clamp_int(pre[t.z], 0, (int)(g.ld / kBK));
+            t.y = pre[t.z];
         } else {
             t = o.at(g, pre, i);
         }
-        if (C::MODE == kWgrad) nk = clamp_int(pre[t.z + 1], t.y, (int)(g.ld / kBK)) - t.y;
+        if (C::MODE == kWgrad) nk = pre[t.z + 1] - t.y;
     }
     __syncthreads();
     if (w.tid < ntiles) {
@@ -809,12 +813,14 @@ __global__ __launch_bounds__(64 * kThinWaves) void k_block_thin(BlockArgs g) {
     } else {
         constexpr int kPer = kMaxGroups / (64 * kThinWaves);
         int first[kPer], n[kPer], sum = 0;
+        bool sound = true;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             first[i] = n[i] = 0;
-            if (tid * kPer + i < g.E) group_rows(g, tid * kPer + i, first[i], n[i]);
+            if (tid * kPer + i < g.E) sound &= group_rows(g, tid * kPer + i, first[i], n[i]);
             sum += (n[i] + MT * 16 - 1) / (MT * 16);
         }
+        if (!__syncthreads_and(sound)) return;
         int before = sum;
         for (int d = 1; d < kWave; d <<= 1) {
             const int up = __shfl_up(before, d);

@@ -926,7 +926,8 @@ __global__ __launch_bounds__(kFinalThreads) void k_balance_final(int T, int E, c
 // ---- host ---------------------------------------------------------------------------
 constexpr int32_t kMaxTokens = 1 << 27;  // a launch holds fewer than 2^32 threads
 bool gate_shape_ok(const moe_gate_shape_t* s) {
-    return s && s->T >= 0 && s->T <= kMaxTokens && s->E >= 1 && s->E <= 1024 && s->K >= 1 && s->K <= 64 && s->K <= s->E;
+    return s && s->T >= 0 && s->T <= kMaxTokens && s->E >= 1 && s->E <= 1024 && s->K >= 1 && s->K <= 64 && s->K <= s->E &&
+           (int64_t)s->T * s->K < (int64_t(1) << 31);
 }
 
 // L * VPL >= E, VPL a power of two; VEC as wide as 16 bytes where every row

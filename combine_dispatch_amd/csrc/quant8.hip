@@ -259,17 +259,21 @@ __global__ __launch_bounds__(kThreads) void k_quantise_columns(const void* __res
         // blocks of experts 4 tid .. 4 tid + 3
         constexpr int kPer = kMaxGroups / kThreads;
         int first[kPer], n[kPer], sum = 0;
+        bool sound = true;  // bounds in order and inside 0..R, else nothing is done
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = tid * kPer + i;
             first[i] = 0;
             n[i] = 0;
             if (e < E) {
-                first[i] = clamp_int(offsets[e], 0, (int)R);
-                n[i] = clamp_int(offsets[e + 1], first[i], (int)R) - first[i];
+                first[i] = offsets[e];
+                const int end = offsets[e + 1];
+                sound &= first[i] >= 0 && first[i] <= end && end <= (int)R;
+                n[i] = end - first[i];
             }
             sum += (n[i] + 127) / 128;
         }
+        if (!__syncthreads_and(sound)) return;
         int before = sum;
         for (int d = 1; d < kWave; d <<= 1) {
             const int up = __shfl_up(before, d);

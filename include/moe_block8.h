@@ -75,8 +75,9 @@ typedef struct {
  * layout with C' = K, w in weights layout with K' = K, 16-byte aligned codes.
  * Each 128-wide block is a matrix-core sum, scaled and added in float32; the
  * result is rounded to bf16 once.  Rows outside offsets[0] .. offsets[E] - 1
- * are left as they are.  offsets NULL: E must be 1, all R rows.  Offsets out
- * of order or range give some result but no access out of bounds.
+ * are left as they are.  offsets NULL: E must be 1, all R rows.  With offsets
+ * out of order or out of 0..R nothing is computed: the output stays as it was
+ * (so too in moe_quantise_columns and moe_block_gemm_wgrad).
  * The gradient by the input is the same product: a = the quantised gradient,
  * w = the transposed weights (codes_t, scales_t), K and N exchanged.
  */

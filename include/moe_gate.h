@@ -32,7 +32,7 @@ enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 typedef struct {
     int32_t T; /* tokens, 0..2^27 */
     int32_t E; /* experts, 1..1024 */
-    int32_t K; /* slots per token, 1..min(E, 64) */
+    int32_t K; /* slots per token, 1..min(E, 64); T * K < 2^31 */
 } moe_gate_shape_t;
 
 typedef struct {

@@ -286,26 +286,27 @@ def test_product_dense_and_rows_outside(moe):
         assert (out[off[1]:off[2]] != -3).any(1).all()
 
 
-def test_products_bad_offsets_stay_in_bounds(moe):
-    R, N, K, E = 150, 64, 128, 3
+@pytest.mark.parametrize("R", [40, 150, 3000])  # split K, small tiles, large tiles
+def test_products_bad_offsets_do_nothing(moe, R):
+    """Out of order or out of range: no call reads past its arrays, none writes."""
+    N, K, E = 64, 128, 3
     ca, sa = ref_rows(data((R, K), torch.bfloat16, 5))
     cw, sw = ref_weights(data((E, N, K), torch.bfloat16, 6))
     cw = cw[:, :N].contiguous().to(DEV)
     Rp = moe.moe_padded_rows(R, E)
-    for off in ([0, 140, 20, 90], [-9, 100, 1 << 30, 5], [1 << 30, 0, 150, -(1 << 31)], [0, 150, 0, 150]):
+    x = data((R, N), torch.bfloat16, 1).to(DEV)
+    for off in ([0, R, 20, R], [-9, R, R, R], [0, 5, 9, R + 1], [1 << 30, 1 << 30, 1 << 30, 1 << 30], [0, R, 0, R],
+                [-(1 << 31), 0, 0, R], [0, 0, 0, (1 << 31) - 1]):
         o = torch.tensor(off, dtype=torch.int32, device=DEV)
-        buf = torch.full((R + 2, N), -3.0, dtype=torch.bfloat16, device=DEV)
-        moe.moe_block_gemm(ca.to(DEV), sa.to(DEV), cw, sw.to(DEV), buf[1:R + 1], offsets=o)
-        assert (buf[0] == -3).all() and (buf[R + 1] == -3).all()
-        codes = torch.full((N + 1, Rp), 77, dtype=torch.uint8, device=DEV)
-        scales = torch.full((Rp // 128 + 1, N), 99, dtype=torch.uint8, device=DEV)
-        x = data((R, N), torch.bfloat16, 1).to(DEV)
-        moe.moe_quantise_columns(x, codes[:N], scales[:Rp // 128], offsets=o)
-        assert (codes[N] == 77).all() and (scales[Rp // 128] == 99).all()
-        dw = torch.full((E * N + 2, N), -3.0, dtype=torch.bfloat16, device=DEV)
-        moe.moe_block_gemm_wgrad(codes[:N], scales[:Rp // 128], codes[:N], scales[:Rp // 128],
-                                 dw[1:E * N + 1].view(E, N, N), rows=R, offsets=o)
-        assert (dw[0] == -3).all() and (dw[E * N + 1] == -3).all()
+        out = torch.full((R, N), -3.0, dtype=torch.bfloat16, device=DEV)
+        moe.moe_block_gemm(ca.to(DEV), sa.to(DEV), cw, sw.to(DEV), out, offsets=o)
+        codes = torch.full((N, Rp), 77, dtype=torch.uint8, device=DEV)
+        scales = torch.full((Rp // 128, N), 99, dtype=torch.uint8, device=DEV)
+        moe.moe_quantise_columns(x, codes, scales, offsets=o)
+        dw = torch.full((E, N, N), -3.0, dtype=torch.bfloat16, device=DEV)
+        moe.moe_block_gemm_wgrad(codes, scales, codes, scales, dw, rows=R, offsets=o)
+        for t, v in ((out, -3), (codes, 77), (scales, 99), (dw, -3)):
+            assert (t == v).all(), off
 
 
 def test_product_of_bad_blocks_is_nan(moe):

@@ -36,7 +36,8 @@ def test_defaults(moe):
 @pytest.mark.parametrize("shape,want", [((-1, 8, 2), "INVALID_ARG"), ((1, 0, 1), "UNSUPPORTED"),
                                         ((1, 1025, 1), "UNSUPPORTED"), ((1, 8, 0), "UNSUPPORTED"),
                                         ((1, 8, 9), "UNSUPPORTED"), ((1, 1024, 65), "UNSUPPORTED"),
-                                        ((1 << 28, 8, 2), "UNSUPPORTED"), ((0, 8, 2), "OK")])
+                                        ((1 << 28, 8, 2), "UNSUPPORTED"),
+                                        ((1 << 27, 64, 16), "UNSUPPORTED"), ((0, 8, 2), "OK")])
 def test_gate_shapes(moe, shape, want):
     st = moe.MOE_OK if want == "OK" else getattr(moe, "MOE_ERR_" + want)
     assert gate(moe, shape) == st
