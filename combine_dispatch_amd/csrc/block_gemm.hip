@@ -502,7 +502,7 @@ __device__ __forceinline__ int plan_tiles(const BlockArgs& g, const Place<C>& w,
     // wgrad, whose groups differ in K steps: an eighth of every group's tiles
     // instead, the largest groups first and the turn reversed every other time,
     // so that XCDs and workgroups get the same work (32 groups of 1024 rows on
-    // average, sizes as rank^-0.6, N 1536, K 2048: 202 us in contiguous eighths, 161 so).
+    // average, sizes as rank^-0.6, N 1536, K 2048: 202 us in contiguous eighths, 153 so).
     const Order<C> o(g, pre);
     const uint32_t xcd = blockIdx.x & 7, turn = blockIdx.x >> 3, step = gridDim.x / 8;
     const uint32_t each = (uint32_t)(o.np * o.nq), lo = each * xcd / 8, share = each * (xcd + 1) / 8 - lo;
@@ -615,7 +615,14 @@ __device__ __forceinline__ void clear_sums(v16f (&acc)[C::J][C::TT], Pending& d)
 // step from LDS, multiply, read the other half, multiply - one phase apart, so
 // that on every SIMD one wave's MFMAs run while the other reads.  The direct
 // loads go out between the MFMAs.  With both waves in the same phase the MFMAs
-// were busy for 51 % of the time.
+// were busy for 51 % of the time (1964 us for the product below, 1808 with the
+// phases apart).
+//
+// Bound by the MFMAs and the power they draw: 65536 rows in 32 groups, N 4096, K
+// 7168 take 1748 us (2.2 PF; the MFMAs busy for 70 % of 2.8 M cycles, the clock
+// at about 1.7 GHz).  In timing copies the scaled adds cost 11 % of that, the loads'
+// issue 21 %, the LDS reads 4 %, the stores 4 %.  One 256 x 256 tile a workgroup, 64 x
+// 128 a wave: 128 KiB of stages and 128 sums a lane fill LDS and registers.
 //
 // Barriers.  Phase f (0..3) of step n lies between barriers 4n + f and
 // 4n + f + 1 for the first waves and one later for the others (they meet once
@@ -717,7 +724,9 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block(
 }
 
 // Few rows a group: the weights' stream bounds it.  64-row tiles, four waves,
-// STAGES K steps in flight, two workgroups on a CU.
+// STAGES K steps in flight, two workgroups on a CU.  1024 rows in 32 groups, N
+// 4096, K 7168: 152 us for 955 MB, 6.3 TB/s (a plain read stream reaches 7.1).
+// One group of 1733 rows, N 1001, K 2048: 13 us, the latency of 16 steps.
 template <class C>
 __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block_few(BlockArgs g) {
     static_assert(C::J == 1 && C::MODE == kProduct && C::STAGES == 3, "");
@@ -791,7 +800,8 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block_
 // it multiplies (few enough registers for two workgroups on a CU: U = 2 beat 4
 // by up to 2x where there are more workgroups than CUs), and the eight partial sums meet in LDS in a fixed order.
 // One v_mfma_f32_16x16x128_f8f6f4 is one block of 128, so the scales apply to
-// its four results.  Bound by the weights' stream and its latency.
+// its four results.  Bound by the weights' stream and its latency: one row, N 4096,
+// K 7168 (29 MB) 9.4 us, 3.1 TB/s, of which about 3 are the launch.
 constexpr int kThinWaves = 8;
 
 template <int MT, int U>
@@ -965,8 +975,12 @@ void launch_thin(const BlockArgs& g, hipStream_t stream) {
 //   7168, N 4096: 48 rows each on average 162 and 206, 64 rows 241 and 210
 //   (every second group needs a second row of small tiles), 128 rows 353 and 223.
 // With at most 64 rows a group and few tiles, K is split instead: a round of
-// one 16-output workgroup per CU takes 0.20, 0.30 or 0.45 us for each K step
-// with 16, 32 or 64 rows.
+// one 16-output workgroup per CU takes 0.15, 0.25 or 0.35 us for each K step
+// with 16, 32 or 64 rows; a grid of small tiles that leaves CUs idle takes 0.375
+// and 3 us more to fill its stages.  Split and small tiles measured: K 7168,
+// N 4096, 1 row 9.4 and 27 us, 32 rows 17 and 27, 64 rows 22 and 28; K 4096,
+// N 8192, 16 rows 13 and 18, 32 rows 21 and 18; 8 groups of 16 rows on average,
+// K 2048, N 1536: 14.5 and 11.9.
 void launch_product(const BlockArgs& g, hipStream_t stream) {
     const int64_t used = g.E < g.R ? g.E : g.R, per = (g.R + used - 1) / used, cus = device_cus();
     const int64_t small = ((g.R + used * 32) / 64 > used ? (g.R + used * 32) / 64 : used) * ((g.N + 127) / 128);
@@ -980,9 +994,11 @@ void launch_product(const BlockArgs& g, hipStream_t stream) {
     const double t_small = std::max(0.54 * (double)(small > cus ? small : cus) / (double)cus, weights * reads / 6.0);
     const double t_large = std::max(1.3 * (double)((large + cus - 1) / cus), weights / 4.4);
     if (per <= 64) {
-        const int64_t thin = (g.offsets ? g.R / 64 + used : 1) * ((g.N + 15) / 16);
-        const double step = per <= 16 ? 0.15 : per <= 32 ? 0.25 : 0.35;
-        if (step * (double)((thin + cus - 1) / cus) < t_small) {
+        const int rows = per <= 16 ? 16 : per <= 32 ? 32 : 64;
+        const int64_t thin = std::max(used, (g.R + used * rows / 2) / rows) * ((g.N + 15) / 16);
+        const double step = per <= 16 ? 0.15 : per <= 32 ? 0.25 : 0.35, nk = (double)(g.K / kBK);
+        const double t_few = small <= cus ? std::max(0.375, weights * reads / 6.0) : t_small;
+        if (step * nk * (double)((thin + cus - 1) / cus) < t_few * nk + 3.0) {
             if (per <= 16) launch_thin<1, 2>(g, stream);
             else if (per <= 32) launch_thin<2, 2>(g, stream);
             else launch_thin<4, 1>(g, stream);

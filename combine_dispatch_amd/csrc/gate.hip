@@ -4,9 +4,14 @@
 // All kernels give one token row to L lanes: lane j keeps VPL = ceil(E / L)
 // logits in registers.  L = 16 (a DPP row): four rows run in a wave and every
 // cross-lane step is four DPP rotations, with no LDS and no barrier.  L = 64
-// (the gate of few tokens): a wave per row, two permlane swaps more.  What bounds them: at training sizes one read of the logits (and
-// one write of the gradient) against HBM; at decode sizes the launch and the
-// chain of K dependent selections.
+// (the gate of few tokens): a wave per row, two permlane swaps more.
+//
+// What bounds them, with times on the GPU: at training sizes the selections' and
+// exponentials' instructions before the read of the logits and the write of the
+// gradient (16384 x 128 float32, softmax, K = 8: gate 8.4 us for 9.4 MB, gradient
+// 5.5 us for 18 MB); at few tokens the launch and the chain of K dependent
+// selections (64 x 256, sigmoid with bias, K = 8: 4.3 us, where an empty kernel
+// takes 2.8; 4099 x 32 bfloat16, K = 2: 3.5 us and 4.1).
 #include "../../include/moe_gate.h"
 #include "moe_device.hpp"
 #include "moe_host.hpp"
@@ -620,7 +625,9 @@ __device__ __forceinline__ float sum_of_rows(float v) {
 }
 
 // One sequence of a small batch: everything in one workgroup and one launch
-// (each of the two launches below is 5 us of latency for any batch).
+// (each of the two launches below is 5 us of latency for any batch).  509 tokens
+// x 32 experts, K = 8: 12.2 us, all latency: the loads, one pass of
+// exponentials, the counts and the barriers of 16 waves.
 constexpr int kOneThreads = 1024;
 template <int DT, int VPL, int VEC>
 __global__ __launch_bounds__(kOneThreads) void k_balance_one(
@@ -689,6 +696,13 @@ __global__ __launch_bounds__(kOneThreads) void k_balance_one(
     }
 }
 
+// The same in two launches: sums and counts of kChunk tokens per workgroup, then
+// of the workgroups per sequence.  No floating-point atomics: partial sums are
+// stored and added in a fixed order, so the loss is the same bits every time.
+// 24 sequences in 16384 tokens x 128 experts, K = 8: 12.9 us (8.4 MB of logits and
+// 1 MB of indices; chunks of 16 and 64 tokens were slower for large and for small
+// batches) and 8.3 us (latency: a workgroup per sequence and block of experts, the
+// last one done adds up the loss).
 template <int DT, int VPL, int VEC>
 __global__ __launch_bounds__(kThreads) void k_balance_part(
     const typename Elem<DT>::type* __restrict__ logits, const uint8_t* __restrict__ mask,
