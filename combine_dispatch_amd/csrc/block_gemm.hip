@@ -446,7 +446,9 @@ struct Frags {
             for (int s = 0; s < 2; ++s)
                 acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(q[j % QSETS][s], p[i][s], acc[j][i], 0, 0, 0,
                                                                             sq[j], 0, sp[i]);
-            asm volatile("" : "+v"(acc[j][i]));
+            // one wave on a SIMD has its sums in the accumulation registers, two have 256 registers in all
+            if constexpr (C::WAVES * C::PER_CU == 4) asm volatile("" : "+a"(acc[j][i]));
+            else asm volatile("" : "+v"(acc[j][i]));
         }
     }
 };
@@ -794,6 +796,94 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block_
     wait_loads<0>();  // no load may write LDS once the workgroup is gone
 }
 
+// wgrad with too few 256 x 256 tiles to fill the GPU (one group above all):
+// 128 x 128 tiles, four waves of 64 x 64, the next step's fragments read under
+// the MFMAs.  One barrier a step: in front of it a wave has read all it needs
+// of this step's stage, so behind it that stage takes the loads of the step
+// STAGES ahead.  Bound by the chain of a step: 64 KB of fragments through LDS and
+// 8 MFMAs a wave with one wave on a SIMD.  64 x 64 a wave reads a fifth less from LDS
+// than 128 x 32 (226 -> 201 us, 32768 rows, N = K = 2048, one group), reading ahead
+// and sums that stay in the accumulation registers 201 -> 180.
+template <class C>
+__global__ __launch_bounds__(C::THREADS, C::WAVES * C::PER_CU / 4) void k_block_square(BlockArgs g) {
+    static_assert(C::J == 2 && C::TT == 2 && C::PP == 4 && C::QP == 4 && C::MODE == kWgrad && C::STAGES >= 3, "");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[C::STAGES * C::STAGE];
+    __shared__ __attribute__((aligned(16))) int table[C::TABLE];
+    __shared__ int wave_sum[C::WAVES];
+    const Place<C> w;
+    const int ntiles = plan_tiles(g, w, table, wave_sum);
+    if (ntiles == 0) return;
+    const TileRec* rec = reinterpret_cast<const TileRec*>(table);
+    const int* steps = table + 4 * C::THREADS;
+
+    const int c = w.lane & 31, h = w.lane >> 5;
+    const int prow = w.wp * 32 * C::TT + c, qrow = w.wq * 32 * C::J + c;
+    const uint32_t pr = prow * kBK + ((h ^ row_key(prow)) << 4);
+    const uint32_t qr = C::QOFF + qrow * kBK + ((h ^ row_key(qrow)) << 4);
+
+    Frags<C> even, odd;
+    const auto read = [&](Frags<C>& f, uint32_t at) {
+        f.read_p(lds, pr + at);
+        f.read_q(lds, qr + at, 0);
+        f.read_q(lds, qr + at, 1);
+    };
+    const uint32_t base = lds_addr(lds);
+    Loader<C> ld(g, w, rec, steps, ntiles);
+    if (ld.left) {
+#pragma unroll
+        for (int s = 0; s < C::STAGES; ++s) {
+            ld.load_all(w, base + s * C::STAGE);
+            ld.advance(g, w, rec, steps, ntiles);
+        }
+        wait_and_meet<C::LOADS*(C::STAGES - 1)>();
+        read(even, 0);
+    }
+    Pending d;
+    uint32_t stage = 0;  // LDS offset of the current step's stage
+    for (int n = 0; n < ntiles; ++n) {
+        Tile<C> t;
+        t.read(g, rec, steps, n);
+        ScaleSkew<C> skew;
+        skew.open(g, t);
+        v16f acc[C::J][C::TT];
+        clear_sums<C>(acc, d);
+        const auto step = [&](Frags<C>& now, Frags<C>& then) {
+            const uint32_t next = stage + C::STAGE == C::STAGES * C::STAGE ? 0u : stage + C::STAGE;
+            now.read_scales(w, lds + stage, skew, prow);
+            wait_and_meet<C::LOADS*(C::STAGES - 2)>();
+            read(then, next);
+            const uint32_t here = base + stage;
+            now.multiply(acc, d, 0, 0);
+            ld.load_p(w, here, 0);
+            ld.load_p(w, here, 1);
+            ld.load_p(w, here, 2);
+            now.multiply(acc, d, 0, 1);
+            ld.load_p(w, here, 3);
+            ld.load_q(w, here, 0);
+            now.multiply(acc, d, 1, 0);
+            ld.load_q(w, here, 1);
+            ld.load_q(w, here, 2);
+            now.multiply(acc, d, 1, 1);
+            ld.load_q(w, here, 3);
+            ld.load_scales(w, here);
+            stage = next;
+            ld.advance(g, w, rec, steps, ntiles);
+            skew.next(g);
+        };
+        int k = 0;
+        for (; k + 1 < t.nk; k += 2) {
+            step(even, odd);
+            step(odd, even);
+        }
+        if (k < t.nk) {
+            step(even, odd);
+            even = odd;
+        }
+        store(g, w, t, acc);
+    }
+    wait_loads<0>();  // no load may write LDS once the workgroup is gone
+}
+
 // A handful of rows and too few tiles to fill the GPU: one workgroup per 16
 // outputs.  Its eight waves share K (wave v takes blocks v, v + 8, ...), each
 // reading its weights and rows straight into registers, U blocks ahead of those
@@ -938,6 +1028,7 @@ typedef Cfg<kProduct, 2, 4, 4, 2, 2, 4, 1> BigProduct;  // 256 x 256, 8 waves of
 template <bool STREAM_Q>
 using SmallProduct = Cfg<kProduct, 4, 1, 1, 2, 3, 1, 2, STREAM_Q>;  // 64 rows x 128, 4 waves of 64 x 32
 typedef Cfg<kWgrad, 2, 4, 4, 2, 2, 4, 1> BigWgrad;
+typedef Cfg<kWgrad, 2, 2, 2, 2, 4, 4, 1> SmallWgrad;  // 128 x 128, 4 waves of 64 x 64
 
 template <class C>
 void launch(const BlockArgs& g, int64_t p_tiles, int q, hipStream_t stream) {
@@ -949,6 +1040,8 @@ void launch(const BlockArgs& g, int64_t p_tiles, int q, hipStream_t stream) {
     if (grid < least) grid = least;
     if constexpr (C::WAVES == 8)
         hipLaunchKernelGGL(k_block<C>, dim3((unsigned)grid), dim3(C::THREADS), 0, stream, g);
+    else if constexpr (C::MODE == kWgrad)
+        hipLaunchKernelGGL(k_block_square<C>, dim3((unsigned)grid), dim3(C::THREADS), 0, stream, g);
     else
         hipLaunchKernelGGL(k_block_few<C>, dim3((unsigned)grid), dim3(C::THREADS), 0, stream, g);
 }
@@ -1019,6 +1112,22 @@ void launch_product(const BlockArgs& g, hipStream_t stream) {
     }
 }
 
+// A K step of a round of tiles (one a CU) takes 1.05 us with 256 x 256 tiles and
+// 0.55 to 0.7 with 128 x 128, so those pay where all of them run at once.  One
+// group of 32768 rows, large and small tiles: N, K = 1024 260 and 143 us, 2048
+// 268 and 180, 2560 x 2048 262 and 295; 4096 rows, 256 x 256 41 and 24.
+void launch_wgrad(const BlockArgs& g, hipStream_t stream) {
+    const auto p_tiles = [&](int bp) { return (int64_t)g.E * ((g.N + bp - 1) / bp); };
+    const int64_t used = g.E < g.R ? g.E : g.R, cus = device_cus();
+    const auto rounds = [&](int b) {
+        return (double)((used * ((g.N + b - 1) / b) * ((g.K + b - 1) / b) + cus - 1) / cus);
+    };
+    if (0.62 * rounds(SmallWgrad::BP) < 1.05 * rounds(BigWgrad::BP))
+        launch<SmallWgrad>(g, p_tiles(SmallWgrad::BP), g.K, stream);
+    else
+        launch<BigWgrad>(g, p_tiles(BigWgrad::BP), g.K, stream);
+}
+
 // An upper bound of the tiles of `p` rows in up to 1024 groups: the kernels count them in 32 bits.
 int64_t tiles(int64_t p, int bp, int64_t q) { return (p / bp + kMaxGroups) * ((q + 127) / 128); }
 bool block_shape_valid(const moe_block_shape_t* s, const int32_t* offsets) {
@@ -1059,7 +1168,7 @@ int moe_block_gemm_wgrad(const moe_block_shape_t* s, const uint8_t* gr, const ui
     if (!device_ok()) return MOE_ERR_DEVICE;
     BlockArgs g = {gr, x, g_scales, x_scales, offsets, static_cast<uint16_t*>(out), s->R, moe_padded_rows(s->R, s->E),
                    s->N, s->K, s->E, s->K % 8 == 0 && aligned(out, 16)};
-    launch<BigWgrad>(g, (int64_t)s->E * ((s->N + BigWgrad::BP - 1) / BigWgrad::BP), s->K, stream);
+    launch_wgrad(g, stream);
     return launch_status();
 }
 

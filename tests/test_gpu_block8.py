@@ -328,7 +328,14 @@ WGRAD = [([1], 8, 8), ([128], 128, 128), ([130], 257, 300), ([0, 300, 0, 5], 130
          ([1] * 20, 64, 136), ([700, 0, 400], 256, 264), ([0, 0], 24, 40)]
 
 
-@pytest.mark.parametrize("sizes,N,K", WGRAD)
+# enough 256 x 256 tiles for the large kernel (the sets above have too few of them), one and two rounds of them
+MIXED = [1, 128, 130, 0, 300, 5, 129, 127, 257, 0, 1, 1, 2, 3, 64, 400, 33]
+# and small tiles of which a workgroup has several, most without rows
+WGRAD_EMPTY = [([0] * 5 + [7] + [0] * 40 + [13] + [0] * 17, 300, 300), ([0] * 150 + [260] + [0] * 149 + [30] + [0] * 6, 100, 72)]
+WGRAD_LARGE = [(MIXED, 700, 760), (MIXED, 760, 761), ([128] + [0, 1, 140] * 13, 701, 768)]
+
+
+@pytest.mark.parametrize("sizes,N,K", WGRAD + WGRAD_LARGE + WGRAD_EMPTY)
 def test_wgrad_exact(moe, sizes, N, K):
     """Values of -1, 0, 1 times a power of two per column: exact sums."""
     R, E = sum(sizes), len(sizes)
@@ -355,7 +362,7 @@ def test_wgrad_exact(moe, sizes, N, K):
         at += n
 
 
-@pytest.mark.parametrize("sizes,N,K", WGRAD[:-1])
+@pytest.mark.parametrize("sizes,N,K", WGRAD[:-1] + WGRAD_LARGE[:2])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_wgrad_random(moe, sizes, N, K, dtype):
     R, E = sum(sizes), len(sizes)
